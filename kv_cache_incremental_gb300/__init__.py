@@ -71,9 +71,11 @@ def _stream_ptr(stream, device):
 
 
 class _DevArray:
-    """Zero-copy __cuda_array_interface__ view of library-owned device memory."""
+    """Zero-copy __cuda_array_interface__ view of library-owned device memory; holds the cache
+    that owns it, and a tensor made from it holds the view, so the memory outlives both."""
 
-    def __init__(self, ptr: int, shape, typestr: str):
+    def __init__(self, ptr: int, shape, typestr: str, owner: "KVCache"):
+        self.owner = owner
         self.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": typestr,
                                          "data": (ptr, False), "version": 3, "strides": None}
 
@@ -186,8 +188,8 @@ class KVCache:
         check(_clib.kv_debug_ring_ptrs(self._h, layer, ctypes.byref(kp), ctypes.byref(vp)))
         dev = f"cuda:{self.device}"
         shape = (self.B, self.Hk, self.R + 1, self.D)
-        K = torch.as_tensor(_DevArray(kp.value, shape, "<i2"), device=dev).view(torch.bfloat16)
-        V = torch.as_tensor(_DevArray(vp.value, shape, "<i2"), device=dev).view(torch.bfloat16)
+        K = torch.as_tensor(_DevArray(kp.value, shape, "<i2", self), device=dev).view(torch.bfloat16)
+        V = torch.as_tensor(_DevArray(vp.value, shape, "<i2", self), device=dev).view(torch.bfloat16)
         return K, V
 
     def copy_rows(self, src: "KVCache", src_rows, dst_rows, keep=None, stream=None) -> None:
@@ -294,8 +296,8 @@ class KVCache:
 
     def storage(self, layer: int):
         """Torch views (K, V) of a layer's storage, [B, Hk, rows, D] bf16; rows = max_len + 1
-        (global, and a hybrid layer's group cache) or R + 1 (sliding).  Zero-copy and valid
-        while the cache lives, except for a paged cache's global layers: there each row's
+        (global, and a hybrid layer's group cache) or R + 1 (sliding).  Zero-copy, valid until
+        the cache is closed (a view keeps it from being collected), except for a paged cache's global layers: there each row's
         blocks are gathered from the pool into a new tensor (slots past the row's blocks are
         zero)."""
         import torch
@@ -305,8 +307,8 @@ class KVCache:
         dev = f"cuda:{self.device}"
         if self.paged_blocks is not None and self.layer_kinds[layer] != KV_SLIDING:
             pool = (self.Hk, self.paged_blocks, 16, self.D)   # head-major pool
-            Kp = torch.as_tensor(_DevArray(kp.value, pool, "<i2"), device=dev).view(torch.bfloat16)
-            Vp = torch.as_tensor(_DevArray(vp.value, pool, "<i2"), device=dev).view(torch.bfloat16)
+            Kp = torch.as_tensor(_DevArray(kp.value, pool, "<i2", self), device=dev).view(torch.bfloat16)
+            Vp = torch.as_tensor(_DevArray(vp.value, pool, "<i2", self), device=dev).view(torch.bfloat16)
             Kp, Vp = Kp.transpose(0, 1), Vp.transpose(0, 1)  # [block][Hk][16][D]
             shape = (self.B, self.Hk, self.max_len + 1, self.D)
             K = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
@@ -322,8 +324,8 @@ class KVCache:
             return K, V
         rows = self.R + 1 if self.layer_kinds[layer] == KV_SLIDING else self.max_len + 1
         shape = (self.B, self.Hk, rows, self.D)
-        K = torch.as_tensor(_DevArray(kp.value, shape, "<i2"), device=dev).view(torch.bfloat16)
-        V = torch.as_tensor(_DevArray(vp.value, shape, "<i2"), device=dev).view(torch.bfloat16)
+        K = torch.as_tensor(_DevArray(kp.value, shape, "<i2", self), device=dev).view(torch.bfloat16)
+        V = torch.as_tensor(_DevArray(vp.value, shape, "<i2", self), device=dev).view(torch.bfloat16)
         return K, V
 
     def block_table(self, row: int):
@@ -345,7 +347,7 @@ class KVCache:
         check(_clib.kv_debug_ptrs(self._h, 0, None, None, ctypes.byref(lp)))
         if not lp.value:
             return None
-        return torch.as_tensor(_DevArray(lp.value, (self.B, self.R), "<i4"),
+        return torch.as_tensor(_DevArray(lp.value, (self.B, self.R), "<i4", self),
                                device=f"cuda:{self.device}")
 
     def debug_wait_timeout(self, limit: int = 4096, stream=None) -> None:
