@@ -346,7 +346,8 @@ enum kv_kernel_kind {
     KV_KERNEL_COMMIT = 4,
     KV_KERNEL_STATE = 5,
     KV_KERNEL_STEP = 6,
-    KV_KERNEL_NKINDS = 7
+    KV_KERNEL_SELECT = 7,   /* block bounds and block selection of sparse attention */
+    KV_KERNEL_NKINDS = 8
 };
 int kv_profile_enable(kv_cache *c, int enable);
 int kv_profile_read(kv_cache *c, int kind, int reset, int64_t *launches, double *total_ms,
@@ -456,6 +457,47 @@ int kv_copy_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
 int64_t kv_export_bytes(const kv_cache *c, int keep);
 int kv_export_row(const kv_cache *c, int row, int keep, void *dst, int64_t bytes, void *stream);
 int kv_import_row(kv_cache *c, int row, int keep, const void *src, int64_t bytes, void *stream);
+
+/*
+ * Sparse attention: a query reads a few blocks of a long cache.  The slots of a global
+ * layer's row are grouped in blocks of 64, from slot 0.  For a query token and kv head the
+ * library attends to the row's first `sink` blocks, to its last `recent` blocks (the one
+ * that holds the token itself included) and to the `top_k` blocks between them with the
+ * largest score; with sink + top_k + recent blocks or fewer it attends to all of them.
+ *
+ * A block's score is an upper bound, in 8-bit levels, on the score of its keys:  per
+ * block and head dimension the smallest and largest key component are kept, rounded
+ * outwards to 127ths of the block's largest magnitude m (lo8 = floor(lo * (127 / m)),
+ * hi8 = ceil(hi * (127 / m)), step = m * (float)(1.0 / 127.0)); a rotated, bf16-rounded
+ * query head is rounded to the nearest of its 127 levels in the same way (q8, qs); the
+ * score is (float)(sum_d max(q8_d lo8_d, q8_d hi8_d)) * (qs * step), in float32
+ * operations, and the block's the largest over the group's Hq / Hk heads.  (A largest
+ * magnitude below 1e-30 counts as 0.)  The sum is a whole number, so the choice does not
+ * depend on the order of additions; ties go to the lower block, NaN scores below all
+ * others.
+ *
+ * kv_sparse_enable: prepares a cache with at least one KV_GLOBAL layer for calls of up to
+ *   max_select (1..4096) blocks per query: allocates, for every global layer, the bounds
+ *   (2 D + 4 bytes per row, kv head and block of 64: 1/128 of the K/V bytes), and block
+ *   lists of 512 x Hk x max_select int32.  Once per cache (KV_ERR_ARG after that),
+ *   KV_ERR_OOM if the memory cannot be had; freed with the cache.  SYNCHRONISES the device.
+ * kv_append_sparse: kv_append on a KV_GLOBAL layer (same q, k, v, n_new, rows, out, effects
+ *   and errors) with the attention above for every new token.  0 <= sink, 0 <= top_k,
+ *   1 <= recent, sink + top_k + recent <= max_select; KV_ERR_ARG otherwise, on a cache that
+ *   is not enabled and on other layer kinds.  `selected` (may be NULL): device int32
+ *   [Bs][C][Hk][sink + top_k + recent], receives each real token's blocks in ascending
+ *   order, then -1; entries of padding tokens are not written.  Bounds of blocks filled by
+ *   any other call (kv_append, copies, imports, step graphs) are computed by the next
+ *   sparse call or update that needs them.
+ * kv_sparse_update: computes the missing bounds of the rows' complete blocks on one global
+ *   layer now (rows NULL: rows 0..n_rows-1), so that the next kv_append_sparse need not,
+ *   e.g. after a prompt went in through kv_append.
+ */
+int kv_sparse_enable(kv_cache *c, int max_select);
+int kv_sparse_update(kv_cache *c, int layer, const int32_t *rows, int n_rows, void *stream);
+int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const void *v, int Hq,
+                     int C, const int32_t *n_new, const int32_t *rows, int Bs, int sink,
+                     int top_k, int recent, void *out, int32_t *selected, void *stream);
 
 /*
  * Decode attention that allocates nothing.  The pages have no counterpart: this

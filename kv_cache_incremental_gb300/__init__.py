@@ -137,6 +137,16 @@ class KVCache:
         if not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
+    def _check_plain(self, x, name, dtype, shape):
+        if x.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
+        if not x.is_cuda or x.device.index != self.device:
+            raise ValueError(f"{name} must live on cuda:{self.device}")
+        if tuple(x.shape) != tuple(shape):
+            raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(x.shape)}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
     # ------------------------------------------------------------------ the path
     def append(self, layer: int, q, k, v, n_new, rows=None, out=None, stream=None):
         """Rotate, append and attend one layer's right-padded chunk; returns out (Bs,C,Hq,D)."""
@@ -179,6 +189,44 @@ class KVCache:
                                     v_local.data_ptr(), ptr(k_global), ptr(v_global), self.Hq,
                                     C, _i32_array(n_new), _i32_array(rows), Bs, out.data_ptr(),
                                     _stream_ptr(stream, q.device)), "kv_append_hybrid")
+        return out
+
+    def enable_sparse(self, max_select: int) -> None:
+        """Prepare append_sparse calls of up to max_select blocks per query; once per cache."""
+        check(_clib.kv_sparse_enable(self._h, max_select), "kv_sparse_enable")
+
+    def update_sparse(self, layer: int, rows=None, stream=None) -> None:
+        """Compute the missing block bounds of rows (default: all) of a global layer now."""
+        n = self.B if rows is None else len(rows)
+        check(_clib.kv_sparse_update(self._h, layer, _i32_array(rows), n,
+                                    _stream_ptr(stream, self.device)), "kv_sparse_update")
+
+    def append_sparse(self, layer: int, q, k, v, n_new, top_k: int, sink: int = 1,
+                      recent: int = 2, rows=None, out=None, selected=None, stream=None):
+        """append() on a global layer, attending to each row's first `sink` and last `recent`
+        blocks of 64 keys and the top_k others with the largest score bounds; selected: an
+        int32 tensor (Bs, C, Hk, sink + top_k + recent) that receives the blocks, -1 past the
+        last.  See kv_append_sparse in include/kvinc.h."""
+        import torch
+        self._check_tensor(q, "q", self.Hq)
+        Bs, C = q.shape[0], q.shape[1]
+        self._check_tensor(k, "k", self.Hk, C, Bs)
+        self._check_tensor(v, "v", self.Hk, C, Bs)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._check_tensor(out, "out", self.Hq, C, Bs)
+        if selected is not None:
+            self._check_plain(selected, "selected", torch.int32,
+                              (Bs, C, self.Hk, sink + top_k + recent))
+        if len(n_new) != Bs or (rows is not None and len(rows) != Bs):
+            raise ValueError("n_new and rows must have one entry per row of q")
+        check(_clib.kv_append_sparse(self._h, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                    self.Hq, C, self._memo_n.get(n_new),
+                                    self._memo_rows.get(rows), Bs, sink, top_k, recent,
+                                    out.data_ptr(),
+                                    None if selected is None else selected.data_ptr(),
+                                    _stream_ptr(stream, q.device)), "kv_append_sparse")
         return out
 
     def ring_storage(self, layer: int):

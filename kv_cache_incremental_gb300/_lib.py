@@ -18,7 +18,7 @@ KV_GLOBAL, KV_SLIDING, KV_HYBRID_FULL, KV_HYBRID_LOCAL = 0, 1, 2, 3
 (KV_OK, KV_ERR_ARG, KV_ERR_FULL, KV_ERR_DTYPE, KV_ERR_CUDA, KV_ERR_OOM, KV_ERR_DEVICE,
  KV_ERR_SCRATCH, KV_ERR_POOL) = range(9)
 KERNELS = {"append": 0, "decode": 1, "combine": 2, "prefill": 3, "commit": 4, "state": 5,
-           "step": 6}
+           "step": 6, "select": 7}
 
 # name -> (restype, argtypes); mirrors include/kvinc.h
 SIGNATURES = {
@@ -74,6 +74,11 @@ SIGNATURES = {
     "kv_export_bytes": (c_int64, [c_void_p, c_int]),
     "kv_export_row": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int64, c_void_p]),
     "kv_import_row": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int64, c_void_p]),
+    "kv_sparse_enable": (c_int, [c_void_p, c_int]),
+    "kv_sparse_update": (c_int, [c_void_p, c_int, P_i32, c_int, c_void_p]),
+    "kv_append_sparse": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                                 P_i32, P_i32, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
+                                 c_void_p]),
     "kv_strerror": (ctypes.c_char_p, [c_int]),
 }
 

@@ -205,7 +205,10 @@ __device__ __forceinline__ void zero_v_chunk(uint8_t *vt, int pstride, int r, in
 // Occupancy is set by shared memory (two CTAs per SM at D = 128, three at D = 64, one with
 // DEEP); the bound tells the register allocator so (left alone it chose 64 registers and
 // spilled at D = 64).
-template <int D, int NT, bool DEEP>
+// LIST: the row's tiles are the blocks of a list (sparse attention, DecodeParams::list); the
+// launch appends nothing, so a tile's masked keys are only the slots past the last block's
+// end.
+template <int D, int NT, bool DEEP, bool LIST>
 __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
     decode_kernel(const __grid_constant__ DecodeParams p) {
   using Cfg = DecodeCfg<D, DEEP>;
@@ -229,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
 
   const int item = blockIdx.x;
   const int g = blockIdx.y;
-  const DecodeRow &row = p.rows[find_item_row(p, item)];
+  const int row_idx = find_item_row(p, item);
+  const DecodeRow &row = p.rows[row_idx];
   // The item's key segment: 0 = the layer storage (a global cache, a sliding ring, or a
   // hybrid layer's group cache), 1 = a hybrid layer's own ring.
   const int split = item - row.item0;          // over all the row's splits (merge slot)
@@ -260,7 +264,64 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
   __syncthreads();  // barriers ready: the producer streams while consumers set up
   const int64_t row0 = ((int64_t)row.cache_row * p.Hk + g) * seg_rows + k0;
 
-  if (warp == kConsumerWarps) {
+  if (LIST && warp == kConsumerWarps) {
+    // ------------------------------------------------------------ producer (listed blocks)
+    // The lanes fetch 32 list entries (and, paged, their table entries) at a time, so that
+    // the tiles' addresses cost one memory round trip per 32 tiles; lane 0 issues the loads.
+    ptx::grid_dep_wait();  // the list comes from the launch before this one
+    const int32_t *list = p.list + ((int64_t)row_idx * p.Hk + g) * p.list_stride + k0 / kTileKeys;
+    const int64_t head0 = ((int64_t)row.cache_row * p.Hk + g) * seg_rows;
+    int4 y4 = make_int4(0, 0, 0, 0);
+    for (int it = 0; it < n_tiles; ++it) {
+      if (it % 32 == 0 && it + lane < n_tiles) {
+        const int blk = list[it + lane];
+        if (pt.max_blocks == 0)
+          y4.x = static_cast<int>(head0 + (int64_t)blk * kTileKeys);
+        else
+          y4 = kv_rows4(pt, row.cache_row, g, blk * kTileKeys);
+      }
+      const int src = it % 32;
+      int4 y;
+      y.x = __shfl_sync(0xffffffffu, y4.x, src);
+      y.y = __shfl_sync(0xffffffffu, y4.y, src);
+      y.z = __shfl_sync(0xffffffffu, y4.z, src);
+      y.w = __shfl_sync(0xffffffffu, y4.w, src);
+      int stop = 0;
+      if (lane == 0) {
+        const int s = it % kStages;
+        if (it >= kStages && !ptx::mbar_wait(&empty[s], ((it / kStages) - 1) & 1, kWaitLimit)) {
+          atomicExch(p.err, 1);  // consumers then give up on the tiles never loaded
+          stop = 1;
+        } else {
+          uint8_t *kt = tiles + s * Cfg::kStageBytes;
+          uint8_t *vt = kt + Cfg::kTileBytes;
+          ptx::mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+          if (pt.max_blocks == 0 || rows4_contiguous(y)) {
+#pragma unroll
+            for (int pn = 0; pn < Cfg::kPanels; ++pn) {
+              ptx::tma_load_2d(kt + pn * kTileKeys * 128, &p.tmap_k, pn * 64, y.x, &full[s]);
+              ptx::tma_load_2d(vt + pn * kTileKeys * 128, &p.tmap_v, pn * 64, y.x, &full[s]);
+            }
+          } else {
+            const int ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < kTileKeys / kBlockTokens; ++j) {
+#pragma unroll
+              for (int pn = 0; pn < Cfg::kPanels; ++pn) {
+                const int off = pn * kTileKeys * 128 + j * kBlockTokens * 128;
+                ptx::tma_load_2d(kt + off, &p.tmap_k16, pn * 64, ys[j], &full[s]);
+                ptx::tma_load_2d(vt + off, &p.tmap_v16, pn * 64, ys[j], &full[s]);
+              }
+            }
+          }
+          *issued = it + 1;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, stop, 0)) break;
+    }
+    return;
+  }
+  if (!LIST && warp == kConsumerWarps) {
     // ------------------------------------------------------------ producer
     // One copy of the loop per segment, so that each names its tensor maps by their
     // fixed parameter addresses.
@@ -629,14 +690,20 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
 
 template <int D, int NT, bool DEEP>
 cudaError_t launch_decode_t(const DecodeParams &p, cudaStream_t s, bool pdl) {
-  return launch_k(decode_kernel<D, NT, DEEP>, dim3(p.n_items, p.Hk), dim3(kThreads),
-                  decode_smem_bytes<D, NT, DEEP>(), s, p, pdl);
+  const dim3 grid(p.n_items, p.Hk), block(kThreads);
+  constexpr int smem = decode_smem_bytes<D, NT, DEEP>();
+  if (p.list) return launch_k(decode_kernel<D, NT, DEEP, true>, grid, block, smem, s, p, pdl);
+  return launch_k(decode_kernel<D, NT, DEEP, false>, grid, block, smem, s, p, pdl);
 }
 
 template <int D, int NT, bool DEEP>
 cudaError_t configure_decode_t() {
   constexpr int smem = decode_smem_bytes<D, NT, DEEP>();
-  return cudaFuncSetAttribute(decode_kernel<D, NT, DEEP>,
+  const cudaError_t e =
+      cudaFuncSetAttribute(decode_kernel<D, NT, DEEP, true>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(decode_kernel<D, NT, DEEP, false>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
@@ -644,10 +711,10 @@ cudaError_t configure_decode_t() {
 template <int D, int NT>
 bool pick_t(bool deep, void **fn, int *smem) {
   if (deep) {
-    *fn = reinterpret_cast<void *>(decode_kernel<D, NT, true>);
+    *fn = reinterpret_cast<void *>(decode_kernel<D, NT, true, false>);
     *smem = decode_smem_bytes<D, NT, true>();
   } else {
-    *fn = reinterpret_cast<void *>(decode_kernel<D, NT, false>);
+    *fn = reinterpret_cast<void *>(decode_kernel<D, NT, false, false>);
     *smem = decode_smem_bytes<D, NT, false>();
   }
   return true;

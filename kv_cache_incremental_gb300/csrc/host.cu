@@ -22,6 +22,7 @@ namespace kvinc {
 cudaError_t configure_decode();
 cudaError_t configure_prefill();
 cudaError_t configure_prefill_tc();
+cudaError_t configure_select();
 cudaError_t launch_prefill_tc(const PrefillParams &p, int D, int tiles, cudaStream_t s,
                               bool pdl);
 int prefill_tc_tiles(int D, int n_rho);
@@ -153,6 +154,19 @@ struct kv_cache {
   // hybrid full layers: per row, lens + the tokens of its last append in this step (a
   // local layer of the group may only append the same tokens after it)
   std::vector<std::vector<int32_t>> hy_end;
+  // sparse attention (kv_sparse_enable): per global layer the 8-bit bounds of every row's
+  // blocks ([B][Hk][nb_cap][2][D], steps [B][Hk][nb_cap]; nullptr elsewhere) and, on the
+  // host, how many of each row's blocks have theirs; the launches' block lists and the
+  // merge tickets of their queries
+  struct Sparse {
+    int max_select = 0;  // 0: not enabled
+    int nb_cap = 0;
+    std::vector<int8_t *> bound;
+    std::vector<float *> scale;
+    std::vector<std::vector<int32_t>> valid;  // [layer][row]
+    int32_t *list = nullptr;                  // [kMaxRowsPerLaunch][Hk][max_select]
+    int32_t *counters = nullptr;              // [kMaxRowsPerLaunch][Hk]
+  } sparse;
   // the cache's last kernel launch (stream, kernel kind or -1 for one that may write any
   // storage, layer) and the layer of the call in progress: a decode launch may stream
   // K/V before its grid dependency wait only when the launch before it on the stream
@@ -237,6 +251,13 @@ int ensure_blocks(kv_cache *c, const std::vector<std::pair<int, int>> &want, cud
   c->last_stream = s;  // table entries: not to be read before a grid dependency wait
   c->last_kind = -1;
   return launch_table(tp, s) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+// The blocks of `row` whose bounds still hold once its first `len` slots are all that is
+// left of what they were computed from.
+void trim_bounds(kv_cache *c, int row, int len) {
+  for (auto &v : c->sparse.valid)
+    if (!v.empty()) v[row] = std::min(v[row], len / kSparseBlock);
 }
 
 // Let go of the blocks of `row` past its first `len` positions (the pool gets back those
@@ -472,6 +493,7 @@ void fill_decode(const kv_cache *c, int layer, const __nv_bfloat16 *q, const __n
   dp.tmap_v16 = c->tmV16[layer];
   dp.fuse_append2 = hybrid ? 1 : 0;
   dp.early_kv = 0;
+  dp.list = nullptr;
   dp.tmap_k2 = hybrid ? c->tmRK[layer] : c->tmK[layer];
   dp.tmap_v2 = hybrid ? c->tmRV[layer] : c->tmV[layer];
   dp.k_new2 = k_local;
@@ -588,6 +610,47 @@ void plan_prefill(const Geom &g, const std::vector<PrefillRow> &prows,
   }
 }
 
+// RoPE + append of the rows `rows_p` of the sub-chunk at token offset `off` of a call's
+// keys and values [Bs][C][Hk][D].
+int launch_append_rows(kv_cache *c, int layer, const __nv_bfloat16 *k, const __nv_bfloat16 *v,
+                       int C, int off, const std::vector<AppendRow> &rows_p, cudaStream_t s) {
+  static thread_local AppendParams ap;
+  const int Hk = c->Hk, D = c->D;
+  for (size_t r0 = 0; r0 < rows_p.size(); r0 += kMaxRowsPerLaunch) {
+    const size_t r1 = std::min(rows_p.size(), r0 + kMaxRowsPerLaunch);
+    ap.k = k + (int64_t)off * Hk * D;
+    ap.v = v + (int64_t)off * Hk * D;
+    ap.kv_row_stride = (int64_t)C * Hk * D;
+    ap.cache_k = (__nv_bfloat16 *)c->K[layer];
+    ap.cache_v = (__nv_bfloat16 *)c->V[layer];
+    ap.scr_k = (__nv_bfloat16 *)c->scrK;
+    ap.scr_v = (__nv_bfloat16 *)c->scrV;
+    ap.rope = c->rope;
+    ap.Hk = Hk;
+    ap.D = D;
+    ap.seg_rows = c->seg_rows[layer];
+    ap.ring_R = c->R;
+    ap.max_len = c->max_len;
+    ap.c_avail = C - off;
+    ap.pt = page_table(c, layer);
+    int blk = 0;
+    double bytes = 0;
+    for (size_t j = r0; j < r1; ++j) {
+      AppendRow r = rows_p[j];
+      r.blk0 = blk;
+      blk += (r.n + 7) / 8;
+      ap.rows[j - r0] = r;
+      bytes += 4.0 * r.n * Hk * D * 2.0;
+    }
+    ap.n_rows = (int)(r1 - r0);
+    ap.n_blocks = blk;
+    cudaError_t e =
+        timed(c, KV_KERNEL_APPEND, bytes, 0, s, [&] { return launch_append(ap, s, c->pdl); });
+    if (e != cudaSuccess) return KV_ERR_CUDA;
+  }
+  return KV_OK;
+}
+
 // One layer's chunk for rows `cache_rows`.  k, v: the keys and values of the layer
 // storage (a hybrid layer: its group's global keys, nullptr on a local layer); kl, vl: a
 // hybrid layer's own local keys and values (its ring), else nullptr.
@@ -623,7 +686,6 @@ int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfl
   }
 
   const int64_t q_row = (int64_t)C * Hq * D, kv_row = (int64_t)C * Hk * D;
-  static thread_local AppendParams ap;
   static thread_local DecodeParams dp;
   static thread_local PrefillParams pp;
   static thread_local CommitParams mp;
@@ -648,37 +710,7 @@ int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfl
     for (int pass = 0; pass < 2; ++pass) {
     const std::vector<AppendRow> &rows_p = pass == 0 ? arows : lrows;
     const __nv_bfloat16 *kp = pass == 0 ? k : kl, *vp = pass == 0 ? v : vl;
-    for (size_t r0 = 0; r0 < rows_p.size(); r0 += kMaxRowsPerLaunch) {
-      const size_t r1 = std::min(rows_p.size(), r0 + kMaxRowsPerLaunch);
-      ap.k = kp + (int64_t)off * Hk * D;
-      ap.v = vp + (int64_t)off * Hk * D;
-      ap.kv_row_stride = kv_row;
-      ap.cache_k = (__nv_bfloat16 *)c->K[layer];
-      ap.cache_v = (__nv_bfloat16 *)c->V[layer];
-      ap.scr_k = (__nv_bfloat16 *)c->scrK;
-      ap.scr_v = (__nv_bfloat16 *)c->scrV;
-      ap.rope = c->rope;
-      ap.Hk = Hk;
-      ap.D = D;
-      ap.seg_rows = c->seg_rows[layer];
-      ap.ring_R = c->R;
-      ap.max_len = c->max_len;
-      ap.c_avail = C - off;
-      ap.pt = page_table(c, layer);
-      int blk = 0;
-      double bytes = 0;
-      for (size_t j = r0; j < r1; ++j) {
-        AppendRow r = rows_p[j];
-        r.blk0 = blk;
-        blk += (r.n + 7) / 8;
-        ap.rows[j - r0] = r;
-        bytes += 4.0 * r.n * Hk * D * 2.0;
-      }
-      ap.n_rows = (int)(r1 - r0);
-      ap.n_blocks = blk;
-      cudaError_t e = timed(c, KV_KERNEL_APPEND, bytes, 0, s, [&] { return launch_append(ap, s, c->pdl); });
-      if (e != cudaSuccess) return KV_ERR_CUDA;
-    }
+    if (launch_append_rows(c, layer, kp, vp, C, off, rows_p, s) != KV_OK) return KV_ERR_CUDA;
     }
 
     // ---- split-K decode for single-token rows (append and split merge fused in)
@@ -865,6 +897,10 @@ void free_all(kv_cache *c) {
   cudaFree(c->ppart_ml);
   cudaFree(c->stage);
   cudaFree(c->table);
+  for (int8_t *p : c->sparse.bound) cudaFree(p);
+  for (float *p : c->sparse.scale) cudaFree(p);
+  cudaFree(c->sparse.list);
+  cudaFree(c->sparse.counters);
   for (auto &r : c->recs) {
     cudaEventDestroy(r.a);
     cudaEventDestroy(r.b);
@@ -906,7 +942,7 @@ static int create_impl(kv_cache **out, int B, int max_len, int Hq, int Hk, int D
   DeviceGuard guard(device);
   if (!get_encode_fn()) return KV_ERR_CUDA;
   if (configure_decode() != cudaSuccess || configure_prefill() != cudaSuccess ||
-      configure_prefill_tc() != cudaSuccess)
+      configure_prefill_tc() != cudaSuccess || configure_select() != cudaSuccess)
     return KV_ERR_CUDA;
 
   kv_cache *c = new kv_cache();
@@ -1117,6 +1153,7 @@ int kv_reset(kv_cache *c, const int32_t *rows, int n_rows, void *stream) {
   for (int r : rv) {
     c->lens[r] = 0;
     release_blocks(c, r, 0);  // later launches on this stream may reuse them
+    trim_bounds(c, r, 0);
     for (auto &he : c->hy_end)
       if (!he.empty()) he[r] = 0;
   }
@@ -2036,6 +2073,7 @@ int kv_copy_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
   for (int i = 0; i < n; ++i) {
     dst->lens[dst_rows[i]] = kp[i];
     release_blocks(dst, dst_rows[i], kp[i]);  // a shortened row gives its tail back
+    trim_bounds(dst, dst_rows[i], in_place(i) ? kp[i] : 0);
     for (auto &he : dst->hy_end)
       if (!he.empty()) he[dst_rows[i]] = kp[i];  // no step in progress
   }
@@ -2143,9 +2181,258 @@ int kv_import_row(kv_cache *c, int row, int keep, const void *src, int64_t bytes
   if (set_ring_state(c, {row}, {keep}, s) != KV_OK) return KV_ERR_CUDA;
   c->lens[row] = keep;
   release_blocks(c, row, keep);
+  trim_bounds(c, row, 0);
   for (auto &he : c->hy_end)
     if (!he.empty()) he[row] = keep;
   return KV_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- sparse attention
+namespace {
+
+// Bounds of the complete blocks of `rows` that have none yet, where row i has `slots[i]`
+// slots filled.  Only blocks below `kept[i]` slots stay known: the slots above are of
+// tokens that a later call of the same step may write again.
+int update_bounds(kv_cache *c, int layer, const std::vector<int32_t> &rows,
+                  const std::vector<int32_t> &slots, const std::vector<int32_t> &kept,
+                  cudaStream_t s) {
+  kv_cache::Sparse &sp = c->sparse;
+  std::vector<int32_t> &valid = sp.valid[layer];
+  static thread_local BoundsParams bp;
+  bp.K = (const __nv_bfloat16 *)c->K[layer];
+  bp.bound = sp.bound[layer];
+  bp.scale = sp.scale[layer];
+  bp.Hk = c->Hk;
+  bp.D = c->D;
+  bp.seg_rows = c->seg_rows[layer];
+  bp.nb_cap = sp.nb_cap;
+  bp.pt = page_table(c, layer);
+  bp.n_rows = bp.n_items = 0;
+  const auto flush = [&] {
+    const double bytes = (double)bp.n_items * c->Hk * c->D * (kSparseBlock * 2.0 + 2.0);
+    const cudaError_t e = timed(c, KV_KERNEL_SELECT, bytes, 0, s,
+                                [&] { return launch_bounds(bp, s, c->pdl); });
+    bp.n_rows = bp.n_items = 0;
+    return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+  };
+  for (size_t i = 0; i < rows.size(); ++i) {
+    const int b0 = valid[rows[i]], b1 = slots[i] / kSparseBlock;
+    if (b1 <= b0) continue;
+    bp.rows[bp.n_rows++] = {rows[i], b0, bp.n_items};
+    bp.n_items += b1 - b0;
+    if (bp.n_rows == kMaxRowsPerLaunch && flush() != KV_OK) return KV_ERR_CUDA;
+  }
+  if (bp.n_rows > 0 && flush() != KV_OK) return KV_ERR_CUDA;
+  for (size_t i = 0; i < rows.size(); ++i)
+    valid[rows[i]] = std::max(valid[rows[i]], kept[i] / kSparseBlock);
+  return KV_OK;
+}
+
+// Selection and attention of up to kMaxRowsPerLaunch queries, tokens [tok0, tok0 + 2^16) of
+// the call's q and out [tok][Hq][D].
+int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat16 *out,
+                    const std::vector<SelectQuery> &qs, int sink, int top_k, int recent,
+                    int32_t *selected, cudaStream_t s) {
+  kv_cache::Sparse &sp = c->sparse;
+  static thread_local SelectParams p;
+  static thread_local DecodeParams dp;
+  const int per = sink + top_k + recent, n = (int)qs.size();
+  const int Hq = c->Hq, Hk = c->Hk, D = c->D;
+  p.q = q;
+  p.rope = c->rope;
+  p.bound = sp.bound[layer];
+  p.scale = sp.scale[layer];
+  p.list = sp.list;
+  p.selected = selected;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rep = Hq / Hk;
+  p.D = D;
+  p.nb_cap = sp.nb_cap;
+  p.list_stride = sp.max_select;
+  p.sink = sink;
+  p.top_k = top_k;
+  p.recent = recent;
+  p.n_queries = n;
+  p.max_cand = 0;
+  double sel_bytes = 0, kv_bytes = 0, flops = 0;
+  const int tok0 = qs[0].tok;
+  for (int i = 0; i < n; ++i) {
+    p.queries[i] = qs[i];
+    const int nb = qs[i].slot / kSparseBlock + 1, n_sel = std::min(nb, per);
+    const int cand = nb > per ? nb - sink - recent : 0;
+    p.max_cand = std::max(p.max_cand, cand);
+    sel_bytes += (double)cand * Hk * (2.0 * D + 4.0);
+    DecodeRow &r = dp.rows[i];
+    r.cache_row = qs[i].cache_row;
+    r.call_row = (uint16_t)(qs[i].tok - tok0);
+    r.pos = qs[i].pos;
+    r.nk = (n_sel - 1) * kSparseBlock + qs[i].slot % kSparseBlock + 1;
+    r.ctr = i;
+    kv_bytes += 4.0 * r.nk * Hk * D;
+    flops += 4.0 * r.nk * Hq * D;
+  }
+  cudaError_t e = timed(c, KV_KERNEL_SELECT, sel_bytes, 0, s,
+                        [&] { return launch_select(p, s, c->pdl); });
+  if (e != cudaSuccess) return KV_ERR_CUDA;
+
+  dp.tmap_k = dp.tmap_k2 = c->tmK[layer];
+  dp.tmap_v = dp.tmap_v2 = c->tmV[layer];
+  dp.tmap_k16 = c->tmK16[layer];
+  dp.tmap_v16 = c->tmV16[layer];
+  dp.q = q + (int64_t)tok0 * Hq * D;
+  dp.out = out + (int64_t)tok0 * Hq * D;
+  dp.q_row_stride = dp.out_row_stride = (int64_t)Hq * D;
+  dp.rope = c->rope;
+  dp.part_o = c->part_o;
+  dp.part_ml = c->part_ml;
+  dp.counters = sp.counters;
+  dp.err = c->err;
+  dp.Hq = Hq;
+  dp.Hk = Hk;
+  dp.rep = Hq / Hk;
+  dp.seg_rows = c->seg_rows[layer];
+  dp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  dp.pt = page_table(c, layer);
+  dp.fuse_append = dp.fuse_append2 = 0;  // appended by a launch before
+  dp.seg0_ring = 0;
+  dp.ring_R = 1;
+  dp.early_kv = 0;
+  dp.list = sp.list;
+  dp.list_stride = sp.max_select;
+  static const int no_ring[kMaxRowsPerLaunch] = {};
+  // the partials are the cache's own: kMaxSplits slots for each of up to min(B, 512) rows
+  plan_decode_splits(c->num_sms, Hk, n, no_ring, dp, std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
+  if (!c->pdl) dp.deep_pipeline = 0;
+  e = timed(c, KV_KERNEL_DECODE, kv_bytes + 4.0 * n * Hq * D, flops, s,
+            [&] { return launch_decode(dp, D, dp.rep <= 8 ? 1 : 2, s, c->pdl); });
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv_sparse_enable(kv_cache *c, int max_select) {
+  if (!c || max_select < 1 || max_select > kMaxSelect || c->sparse.max_select) return KV_ERR_ARG;
+  bool any = false;
+  for (int k : c->kind) any |= k == KV_GLOBAL;
+  if (!any) return KV_ERR_ARG;
+  DeviceGuard guard(c->device);
+  kv_cache::Sparse sp;
+  sp.nb_cap = std::max(1, c->max_len / kSparseBlock);
+  const size_t blocks = (size_t)c->B * c->Hk * sp.nb_cap;
+  bool ok = true;
+  for (int l = 0; l < c->n_layers; ++l) {
+    void *b = nullptr, *f = nullptr;
+    if (c->kind[l] == KV_GLOBAL) {
+      ok = ok && cudaMalloc(&b, blocks * 2 * c->D) == cudaSuccess;
+      ok = ok && cudaMalloc(&f, blocks * 4) == cudaSuccess;
+    }
+    sp.bound.push_back((int8_t *)b);
+    sp.scale.push_back((float *)f);
+    sp.valid.push_back(std::vector<int32_t>(c->kind[l] == KV_GLOBAL ? c->B : 0, 0));
+  }
+  const size_t queries = (size_t)kMaxRowsPerLaunch * c->Hk;
+  ok = ok && cudaMalloc((void **)&sp.list, queries * max_select * 4) == cudaSuccess;
+  ok = ok && cudaMalloc((void **)&sp.counters, queries * 4) == cudaSuccess;
+  const bool have = ok;
+  ok = ok && cudaMemset(sp.counters, 0, queries * 4) == cudaSuccess &&
+       cudaDeviceSynchronize() == cudaSuccess;
+  if (!ok) {
+    for (int8_t *p : sp.bound) cudaFree(p);
+    for (float *p : sp.scale) cudaFree(p);
+    cudaFree(sp.list);
+    cudaFree(sp.counters);
+    cudaGetLastError();
+    return have ? KV_ERR_CUDA : KV_ERR_OOM;
+  }
+  sp.max_select = max_select;
+  c->sparse = sp;
+  return KV_OK;
+}
+
+int kv_sparse_update(kv_cache *c, int layer, const int32_t *rows, int n_rows, void *stream) {
+  if (!c || layer < 0 || layer >= c->n_layers || c->kind[layer] != KV_GLOBAL ||
+      !c->sparse.max_select || n_rows < 0 || n_rows > c->B)
+    return KV_ERR_ARG;
+  std::vector<char> seen(c->B, 0);
+  std::vector<int32_t> rv, slots;
+  for (int i = 0; i < n_rows; ++i) {
+    const int r = rows ? rows[i] : i;
+    if (r < 0 || r >= c->B || seen[r]) return KV_ERR_ARG;
+    seen[r] = 1;
+    rv.push_back(r);
+    slots.push_back(c->lens[r]);
+  }
+  DeviceGuard guard(c->device);
+  c->cur_layer = layer;
+  return update_bounds(c, layer, rv, slots, slots, (cudaStream_t)stream);
+}
+
+int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const void *v, int Hq,
+                     int C, const int32_t *n_new, const int32_t *rows, int Bs, int sink,
+                     int top_k, int recent, void *out, int32_t *selected, void *stream) {
+  if (!c || layer < 0 || layer >= c->n_layers || Hq != c->Hq || C < 1) return KV_ERR_ARG;
+  if (c->kind[layer] != KV_GLOBAL || sink < 0 || top_k < 0 || recent < 1 ||
+      (int64_t)sink + top_k + recent > c->sparse.max_select)
+    return KV_ERR_ARG;
+  std::vector<int32_t> cache_rows;
+  int rc = check_rows(c, n_new, rows, Bs, C, cache_rows);
+  if (rc != KV_OK) return rc;
+  int max_n = 0;
+  for (int i = 0; i < Bs; ++i) max_n = std::max(max_n, (int)n_new[i]);
+  if (max_n == 0) return KV_OK;
+  if (!q || !k || !v || !out || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(out) || (reinterpret_cast<uintptr_t>(selected) & 3u) ||
+      (int64_t)Bs * C >= (1LL << 31))
+    return KV_ERR_ARG;
+  DeviceGuard guard(c->device);
+  cudaStream_t s = (cudaStream_t)stream;
+  c->cur_layer = layer;
+  std::vector<std::pair<int, int>> want;
+  std::vector<int32_t> live, slots, kept;
+  for (int i = 0; i < Bs; ++i) {
+    if (n_new[i] == 0) continue;
+    const int r = cache_rows[i];
+    want.push_back({r, c->lens[r] + n_new[i]});
+    live.push_back(r);
+    slots.push_back(c->lens[r] + n_new[i]);
+    kept.push_back(c->lens[r]);
+  }
+  rc = ensure_blocks(c, want, s);  // before anything else is enqueued
+  if (rc != KV_OK) return rc;
+  for (int off = 0; off < max_n; off += kChunk) {
+    std::vector<AppendRow> arows;
+    for (int i = 0; i < Bs; ++i)
+      if (n_new[i] > off)
+        arows.push_back({cache_rows[i], i, c->lens[cache_rows[i]] + off,
+                         std::min(kChunk, n_new[i] - off), kDestGlobal, 0});
+    rc = launch_append_rows(c, layer, (const __nv_bfloat16 *)k, (const __nv_bfloat16 *)v, C, off,
+                            arows, s);
+    if (rc != KV_OK) return rc;
+  }
+  rc = update_bounds(c, layer, live, slots, kept, s);
+  if (rc != KV_OK) return rc;
+  // queries in launches of at most kMaxRowsPerLaunch, whose tokens lie within 2^16 of the
+  // first one's (the kernels' 16-bit token index)
+  std::vector<SelectQuery> batch;
+  for (int i = 0; i < Bs; ++i)
+    for (int t = 0; t < n_new[i]; ++t) {
+      const int pos = c->lens[cache_rows[i]] + t, tok = i * C + t;
+      if (!batch.empty() &&
+          ((int)batch.size() == kMaxRowsPerLaunch || tok - batch[0].tok > 0xffff)) {
+        rc = attend_selected(c, layer, (const __nv_bfloat16 *)q, (__nv_bfloat16 *)out, batch, sink,
+                             top_k, recent, selected, s);
+        if (rc != KV_OK) return rc;
+        batch.clear();
+      }
+      batch.push_back({cache_rows[i], pos, pos, tok});
+    }
+  return attend_selected(c, layer, (const __nv_bfloat16 *)q, (__nv_bfloat16 *)out, batch, sink,
+                         top_k, recent, selected, s);
 }
 
 const char *kv_strerror(int code) {

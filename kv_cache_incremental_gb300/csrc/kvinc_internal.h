@@ -165,6 +165,12 @@ struct DecodeParams {  // 64-byte aligned through its CUtensorMap members
   // Host only: the launch fits one wave (n_items x Hk <= the SM count), so it runs the
   // variant with twice the K/V stages and one CTA per SM.
   int deep_pipeline;
+  // Sparse attention (the list variant of the kernel): tile t of row r's keys for kv head g
+  // is block list[(r * Hk + g) * list_stride + t] of the row's storage slots, and nk, splits
+  // and tiles count in that list.  The last listed block is the only one that may be partly
+  // filled.  nullptr: tile t is slots [64 t, 64 t + 64).
+  const int32_t *list;
+  int list_stride;
   DecodeRow rows[kMaxRowsPerLaunch];
 };
 
@@ -292,6 +298,49 @@ struct TableParams {
   int32_t row[kMaxTableEntries], idx[kMaxTableEntries], blk[kMaxTableEntries];
 };
 
+// ---------------------------------------------------------------- sparse attention
+// Keys of a block that sparse attention selects as one; a K/V tile of the decode kernel.
+constexpr int kSparseBlock = kTileKeys;
+// Largest number of blocks one query may select (sink + top_k + recent).
+constexpr int kMaxSelect = 4096;
+
+// 8-bit bounds of the blocks [blk0, blk0 + n_blk) of a row, for every kv head.
+struct BoundsRow {
+  int32_t cache_row;
+  int32_t blk0;
+  int32_t item0;  // first block of this row in the launch
+};
+struct BoundsParams {
+  const __nv_bfloat16 *K;  // layer storage
+  int8_t *bound;           // [B][Hk][nb_cap][2][D]: upper bounds, then lower ones
+  float *scale;            // [B][Hk][nb_cap]
+  int Hk, D, seg_rows, nb_cap;
+  PageTable pt;
+  int n_rows, n_items;
+  BoundsRow rows[kMaxRowsPerLaunch];
+};
+
+// One query token: its blocks, per kv head, in ascending order.
+struct SelectQuery {
+  int32_t cache_row;
+  int32_t slot;  // storage slot of the token's own key
+  int32_t pos;   // its position
+  int32_t tok;   // its index in q and `selected`
+};
+struct SelectParams {
+  const __nv_bfloat16 *q;  // [tok][Hq][D], pre-RoPE
+  const float2 *rope;
+  const int8_t *bound;     // as BoundsParams
+  const float *scale;
+  int32_t *list;           // [query of the launch][Hk][list_stride]
+  int32_t *selected;       // [tok][Hk][sink + top_k + recent] or nullptr
+  int Hq, Hk, rep, D, nb_cap, list_stride;
+  int sink, top_k, recent;
+  int n_queries;
+  int max_cand;            // most candidate blocks of a query of the launch
+  SelectQuery queries[kMaxRowsPerLaunch];
+};
+
 // ---------------------------------------------------------------- launchers
 // Launch kernel(p) on s.  With pdl, as a programmatic dependent launch: the grid may start
 // while the previous kernel on the stream finishes, and waits for it (griddepcontrol.wait)
@@ -344,6 +393,8 @@ cudaError_t launch_prefill(const PrefillParams &p, int D, cudaStream_t s, bool p
 cudaError_t launch_prefill_merge(const MergeParams &p, int D, cudaStream_t s, bool pdl = false);
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_state(const StateParams &p, cudaStream_t s, bool pdl = false);
+cudaError_t launch_bounds(const BoundsParams &p, cudaStream_t s, bool pdl = false);
+cudaError_t launch_select(const SelectParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_wait_probe(int32_t *err, uint32_t limit, cudaStream_t s);
 // Opt kernels into their dynamic shared memory sizes (once per process and device).
 cudaError_t configure_kernels();
@@ -357,6 +408,8 @@ static_assert(sizeof(CommitParams) <= kMaxParamBytes, "commit parameters too lar
 static_assert(sizeof(CopyParams) <= kMaxParamBytes, "copy parameters too large");
 static_assert(sizeof(TableParams) <= kMaxParamBytes, "table parameters too large");
 static_assert(sizeof(StateParams) <= kMaxParamBytes, "state parameters too large");
+static_assert(sizeof(BoundsParams) <= kMaxParamBytes, "bounds parameters too large");
+static_assert(sizeof(SelectParams) <= kMaxParamBytes, "select parameters too large");
 static_assert(sizeof(MergeParams) <= kMaxParamBytes, "merge parameters too large");
 
 }  // namespace kvinc
