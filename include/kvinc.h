@@ -347,7 +347,9 @@ enum kv_kernel_kind {
     KV_KERNEL_STATE = 5,
     KV_KERNEL_STEP = 6,
     KV_KERNEL_SELECT = 7,   /* block bounds and block selection of sparse attention */
-    KV_KERNEL_NKINDS = 8
+    KV_KERNEL_WEIGHTS = 8,  /* per-key attention weights */
+    KV_KERNEL_EVICT = 9,    /* the choice and the moves of an eviction */
+    KV_KERNEL_NKINDS = 10
 };
 int kv_profile_enable(kv_cache *c, int enable);
 int kv_profile_read(kv_cache *c, int kind, int reset, int64_t *launches, double *total_ms,
@@ -498,6 +500,62 @@ int kv_sparse_update(kv_cache *c, int layer, const int32_t *rows, int n_rows, vo
 int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const void *v, int Hq,
                      int C, const int32_t *n_new, const int32_t *rows, int Bs, int sink,
                      int top_k, int recent, void *out, int32_t *selected, void *stream);
+
+/*
+ * Eviction from the full-length caches by accumulated attention weight.
+ *
+ * kv_append_weights: kv_append on a KV_GLOBAL layer (same q, k, v, n_new, rows, out, effects
+ *   and errors) that also counts which keys the new tokens attend to.  acc_in, acc_out:
+ *   device float [B][Hk][max_len], an accumulator per cache row, kv head and storage slot
+ *   that the caller owns, 4-byte aligned; the same buffer, or two that do not overlap.  For
+ *   every row with n = n_new[i] > 0 and slots s before the call, kv head g and slot
+ *   j < s + n:
+ *     acc_out[row][g][j] = (j < s ? acc_in[row][g][j] : 0)
+ *                          + sum of the softmax weights that key j gets from the heads
+ *                            h / (Hq / Hk) == g of the row's last min(n, last) new tokens.
+ *   Other entries of acc_out (rows without new tokens, slots j >= s + n) are not written, so
+ *   nothing has to be cleared when a row starts over.  last >= 1; a prompt's chunk may count
+ *   its last few queries only.  Sums are in float, in an order that does not vary between
+ *   runs.  KV_ERR_ARG on other layer kinds; KV_ERR_SCRATCH if Hq exceeds the reserved
+ *   prefill partials (see kv_cache_create).
+ *
+ * kv_evict_rows: for i < n, destination row dst_rows[i] of `dst` becomes source row
+ *   src_rows[i] of `src` with at most `keep` of its keys on every global layer: per layer and
+ *   kv head its last `recent` slots and, of the others, the keep - recent with the largest
+ *   acc_in (ties: the lower slot; NaN counts below every number), in ascending order at slots
+ *   0..keep-1.  A row with keep slots or fewer keeps them all.  Sliding layers keep their
+ *   rings.  The row's length and positions do not change: a later token is rotated at its
+ *   true position, attends to the kept keys at theirs, and goes to the next free slot
+ *   (kv_get_slots), while kv_append and the other calls that append go on as before.
+ *   acc_in: host array [n_layers] of device float [src B][Hk][src max_len], set for the
+ *     global layers (entries of others are ignored).
+ *   acc_out: NULL, or such an array for `dst` ([dst B][Hk][dst max_len]) with NULL where
+ *     not wanted: the kept keys' accumulators, moved with them.  acc_out[l] may be acc_in[l]
+ *     when dst == src; else the two must not overlap.
+ *   kept: host array [n_layers] of device int32 [n][Hk][keep], set for the global layers:
+ *     receives the source slots of destination slots 0.., -1 past the last.
+ *   1 <= keep <= both caches' max_len, 0 <= recent <= keep.  dst may be src, and a row its
+ *   own destination (cut in place; a paged row's blocks past the kept keys return to the
+ *   pool; blocks that other rows hold too are copied first, which takes free blocks).  Rows,
+ *   layouts and rings as for kv_copy_rows, the source rows copied at their whole length;
+ *   KV_ERR_ARG for violations, caches without global layers or with hybrid ones, KV_ERR_POOL
+ *   as for the other calls, before anything is enqueued.  Asynchronous on `stream`.  Called
+ *   between steps: tokens appended but not yet advanced over are not among a row's keys.
+ *   A row with evicted keys cannot be the source of kv_copy_rows or kv_export_row
+ *   (KV_ERR_ARG): its slots are not its first positions.  It may be evicted again, into any
+ *   row.  kv_reset, kv_import_row and copies into it make it an ordinary row again.
+ *
+ * kv_get_slots: keys each row holds in the full-length caches (host int32 [B]): its length
+ *   less the keys evicted from it.  No device sync.
+ */
+int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, const void *v, int Hq,
+                      int C, const int32_t *n_new, const int32_t *rows, int Bs, int last,
+                      const float *acc_in, float *acc_out, void *out, void *stream);
+int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
+                  const int32_t *src_rows, int n, int keep, int recent,
+                  const float *const *acc_in, float *const *acc_out, int32_t *const *kept,
+                  void *stream);
+int kv_get_slots(const kv_cache *c, int32_t *slots_out);
 
 /*
  * Decode attention that allocates nothing.  The pages have no counterpart: this

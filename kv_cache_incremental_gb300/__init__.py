@@ -229,6 +229,75 @@ class KVCache:
                                     _stream_ptr(stream, q.device)), "kv_append_sparse")
         return out
 
+    def append_weights(self, layer: int, q, k, v, n_new, acc_in, acc_out, last=None, rows=None,
+                       out=None, stream=None):
+        """append() on a global layer that adds the softmax weights of each row's last `last`
+        (default: all) new tokens to a per-key accumulator: float32 tensors (B, Hk, max_len),
+        acc_out = acc_in (0 for the new keys) + weights; the same tensor or two that do not
+        overlap.  See kv_append_weights in include/kvinc.h."""
+        import torch
+        self._check_tensor(q, "q", self.Hq)
+        Bs, C = q.shape[0], q.shape[1]
+        self._check_tensor(k, "k", self.Hk, C, Bs)
+        self._check_tensor(v, "v", self.Hk, C, Bs)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._check_tensor(out, "out", self.Hq, C, Bs)
+        for x, name in ((acc_in, "acc_in"), (acc_out, "acc_out")):
+            self._check_plain(x, name, torch.float32, (self.B, self.Hk, self.max_len))
+        if len(n_new) != Bs or (rows is not None and len(rows) != Bs):
+            raise ValueError("n_new and rows must have one entry per row of q")
+        check(_clib.kv_append_weights(self._h, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                     self.Hq, C, self._memo_n.get(n_new),
+                                     self._memo_rows.get(rows), Bs, C if last is None else last,
+                                     acc_in.data_ptr(), acc_out.data_ptr(), out.data_ptr(),
+                                     _stream_ptr(stream, q.device)), "kv_append_weights")
+        return out
+
+    def evict_rows(self, src: "KVCache", src_rows, dst_rows, keep: int, recent: int, acc,
+                   acc_out=None, kept=None, stream=None):
+        """Rows dst_rows of this cache become rows src_rows of `src` (this cache or another of
+        the same layout) with at most `keep` keys per global layer: the last `recent` and the
+        heaviest others by acc[layer] (float32 (src.B, Hk, src.max_len), None on other
+        layers).  acc_out[layer] (float32 (B, Hk, max_len) or None) receives the kept keys'
+        accumulators, kept[layer] (int32 (n, Hk, keep), made when not given) their source
+        slots.  Returns kept.  See kv_evict_rows in include/kvinc.h."""
+        import torch
+        n, L = len(src_rows), len(self.layer_kinds)
+        if len(dst_rows) != n:
+            raise ValueError("src_rows and dst_rows need one entry per row")
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if kept is None:
+            with torch.cuda.stream(stream):
+                kept = [torch.empty((n, self.Hk, max(keep, 0)), dtype=torch.int32,
+                                    device=f"cuda:{self.device}") if kind == KV_GLOBAL else None
+                        for kind in self.layer_kinds]
+        lists = [acc, [None] * L if acc_out is None else acc_out, kept]
+        for xs, name, dtype, shape in (
+                (lists[0], "acc", torch.float32, (src.B, src.Hk, src.max_len)),
+                (lists[1], "acc_out", torch.float32, (self.B, self.Hk, self.max_len)),
+                (lists[2], "kept", torch.int32, (n, self.Hk, keep))):
+            if len(xs) != L:
+                raise ValueError(f"{name}: one entry per layer ({L})")
+            for l, x in enumerate(xs):
+                if x is None and self.layer_kinds[l] == KV_GLOBAL and name != "acc_out":
+                    raise ValueError(f"{name}[{l}]: a global layer needs a tensor")
+                if x is not None:
+                    self._check_plain(x, f"{name}[{l}]", dtype, shape)
+        ptrs = [(ctypes.c_void_p * L)(*[None if x is None else x.data_ptr() for x in xs])
+                for xs in lists]
+        check(_clib.kv_evict_rows(self._h, _i32_array(dst_rows), src._h, _i32_array(src_rows), n,
+                                 keep, recent, *ptrs, _stream_ptr(stream, self.device)),
+              "kv_evict_rows")
+        return kept
+
+    def evict(self, rows, keep: int, recent: int, acc, kept=None, stream=None):
+        """Cut rows in place to at most `keep` keys per global layer; acc[layer] moves along."""
+        return self.evict_rows(self, rows, rows, keep, recent, acc, acc_out=acc, kept=kept,
+                               stream=stream)
+
     def ring_storage(self, layer: int):
         """Zero-copy torch views (K, V) of a hybrid layer's ring, [B, Hk, R + 1, D] bf16."""
         import torch
@@ -337,6 +406,13 @@ class KVCache:
     def lens(self):
         arr = (ctypes.c_int32 * self.B)()
         check(_clib.kv_get_lens(self._h, arr))
+        return list(arr)
+
+    @property
+    def slots(self):
+        """Keys each row holds in the full-length caches: its length less evicted keys."""
+        arr = (ctypes.c_int32 * self.B)()
+        check(_clib.kv_get_slots(self._h, arr))
         return list(arr)
 
     def nbytes(self) -> int:

@@ -18,7 +18,7 @@ KV_GLOBAL, KV_SLIDING, KV_HYBRID_FULL, KV_HYBRID_LOCAL = 0, 1, 2, 3
 (KV_OK, KV_ERR_ARG, KV_ERR_FULL, KV_ERR_DTYPE, KV_ERR_CUDA, KV_ERR_OOM, KV_ERR_DEVICE,
  KV_ERR_SCRATCH, KV_ERR_POOL) = range(9)
 KERNELS = {"append": 0, "decode": 1, "combine": 2, "prefill": 3, "commit": 4, "state": 5,
-           "step": 6, "select": 7}
+           "step": 6, "select": 7, "weights": 8, "evict": 9}
 
 # name -> (restype, argtypes); mirrors include/kvinc.h
 SIGNATURES = {
@@ -79,6 +79,12 @@ SIGNATURES = {
     "kv_append_sparse": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                  P_i32, P_i32, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
                                  c_void_p]),
+    "kv_append_weights": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                                  P_i32, P_i32, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                  c_void_p]),
+    "kv_evict_rows": (c_int, [c_void_p, P_i32, c_void_p, P_i32, c_int, c_int, c_int]
+                      + [ctypes.POINTER(c_void_p)] * 3 + [c_void_p]),
+    "kv_get_slots": (c_int, [c_void_p, P_i32]),
     "kv_strerror": (ctypes.c_char_p, [c_int]),
 }
 

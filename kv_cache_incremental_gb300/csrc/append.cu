@@ -83,10 +83,10 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
       const int t = t0 + tl;
       if (u >= units || t >= c_avail) continue;  // beyond the caller's tensor: nothing to route
       const bool real = t < row.n;
-      const int pos = row.lens + t;
+      const int pos = row.lens + t;  // slot, or a ring's position
       const uint4 k1 = in[i][0], k2 = in[i][1], v1 = in[i][2], v2 = in[i][3];
       uint4 o1 = k1, o2 = k2;  // padding keys are routed unrotated
-      if (real) rope8(k1, k2, p.rope + (int64_t)pos * half + 8 * c, o1, o2);
+      if (real) rope8(k1, k2, p.rope + (int64_t)(pos + row.shift) * half + 8 * c, o1, o2);
 
       __nv_bfloat16 *dk, *dv;
       int64_t dst;

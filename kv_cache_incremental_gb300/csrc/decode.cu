@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
   const int k0 = ssplit * split_len;
   const int k1 = min(seg1 ? min(row.pos + 1, p.ring_R) : row.nk, k0 + split_len);
   const int n_tiles = (k1 - k0 + kTileKeys - 1) / kTileKeys;
-  const int new_slot = seg1 || p.seg0_ring ? row.pos % p.ring_R : row.pos;
+  // a cache's new key comes after the row's others (at slot pos unless keys were evicted)
+  const int new_slot = seg1 || p.seg0_ring ? row.pos % p.ring_R : row.nk - 1;
   const bool owner = (seg1 ? p.fuse_append2 : p.fuse_append) && new_slot >= k0 && new_slot < k1;
   const int seg_rows = seg1 ? p.seg_rows2 : p.seg_rows;
   PageTable pt = p.pt;

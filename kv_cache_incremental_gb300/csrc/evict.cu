@@ -1,0 +1,236 @@
+// evict.cu -- eviction: which keys of a row stay, and moving them together.
+//
+// Per (row, global layer, kv head) the last `recent` of the row's keys stay, and of the
+// others the keep - recent with the largest accumulated weight (ties: the lower slot; NaN
+// below every number).  The kept keys keep their order: destination slot i takes the i-th
+// smallest kept slot, so that "recent" still means the last slots afterwards.
+//
+// The choice is a radix selection: the (keep - recent)-th largest weight is found 11, 11
+// and 10 bits at a time from histograms of the order-preserving whole numbers of the
+// weights, then the slots above it (and the first of its ties) are written in order from
+// per-warp counts.  One CTA per (row, layer, kv head); the numbers stay in shared memory
+// while they fit.
+#include "kvinc_internal.h"
+#include "ptx.cuh"
+
+namespace kvinc {
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+// Weights held in shared memory at most (192 KB); a longer row's are read again per pass.
+constexpr int kHeld = 48 * 1024;
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0;
+  const uint32_t u = __float_as_uint(x + 0.f);  // -0 as +0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+template <bool HELD>
+__global__ void __launch_bounds__(kThreads)
+    evict_select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ uint32_t held[];
+  __shared__ int hist[kBins];
+  __shared__ int warp_n[kWarps][2];
+  __shared__ int pick[2];
+  const EvictItem &it = p.items[blockIdx.x];
+  const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float *acc = it.acc_in + (int64_t)g * p.acc_in_stride;
+  int32_t *kept = it.kept + (int64_t)g * p.keep;
+  const int m = min(it.slots, p.keep);
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if (it.slots <= p.keep) {
+    for (int i = tid; i < p.keep; i += kThreads) kept[i] = i < it.slots ? i : -1;
+  } else {
+    const int n = it.slots - p.recent, want = p.keep - p.recent;
+    for (int i = tid; i < p.recent; i += kThreads) kept[want + i] = n + i;
+    if (HELD)
+      for (int i = tid; i < n; i += kThreads) held[i] = order_key(acc[i]);
+    const auto key_at = [&](int i) { return HELD ? held[i] : order_key(acc[i]); };
+    if (want > 0) {
+      uint32_t prefix = 0, mask = 0;
+      int above = 0;
+      for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const int bins = pass == 2 ? 1024 : 2048;
+        for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+          const uint32_t k = key_at(i);
+          if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {  // from the largest bin down, bins / 32 per lane
+          const int span = bins / 32, top = bins - 1 - span * lane;
+          int sum = 0;
+          for (int i = 0; i < span; ++i) sum += hist[top - i];
+          int incl = sum;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += x;
+          }
+          int run = above + incl - sum;
+          if (run < want && above + incl >= want)
+            for (int i = 0; i < span; ++i) {
+              const int c = hist[top - i];
+              if (run + c >= want) {
+                pick[0] = top - i;
+                pick[1] = run;
+                break;
+              }
+              run += c;
+            }
+        }
+        __syncthreads();
+        prefix |= (uint32_t)pick[0] << shift;
+        mask |= (uint32_t)(bins - 1) << shift;
+        above = pick[1];
+      }
+      // Each warp writes the kept slots of one contiguous range, after those of the warps
+      // before it.
+      const int ties = want - above;
+      const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
+      const int a = min(warp * per, n), b = min(a + per, n);
+      int gt = 0, eq = 0;
+      for (int i = a + lane; i < b; i += 32) {
+        const uint32_t k = key_at(i);
+        gt += k > prefix;
+        eq += k == prefix;
+      }
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        gt += __shfl_xor_sync(0xffffffffu, gt, off);
+        eq += __shfl_xor_sync(0xffffffffu, eq, off);
+      }
+      if (lane == 0) {
+        warp_n[warp][0] = gt;
+        warp_n[warp][1] = eq;
+      }
+      __syncthreads();
+      gt = eq = 0;
+      for (int w = 0; w < warp; ++w) {
+        gt += warp_n[w][0];
+        eq += warp_n[w][1];
+      }
+      const uint32_t below = (1u << lane) - 1;
+      for (int i0 = a; i0 < b; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < b ? key_at(i) : 0;
+        const bool is_gt = i < b && k > prefix, is_eq = i < b && k == prefix;
+        const uint32_t bg = __ballot_sync(0xffffffffu, is_gt);
+        const uint32_t be = __ballot_sync(0xffffffffu, is_eq);
+        const int ng = gt + __popc(bg & below), ne = eq + __popc(be & below);
+        if (is_gt || (is_eq && ne < ties)) kept[ng + min(ne, ties)] = i;
+        gt += __popc(bg);
+        eq += __popc(be);
+      }
+    }
+  }
+  if (!it.acc_out) return;
+  // The kept accumulators, moved together.  acc_out may be acc_in: a kept slot never lies
+  // below its destination, so what a pass writes has been read by it or an earlier one.
+  float *out = it.acc_out + (int64_t)g * p.acc_out_stride;
+  __syncthreads();
+  for (int i0 = 0; i0 < m; i0 += kThreads) {
+    const int i = i0 + tid;
+    const float x = i < m ? acc[kept[i]] : 0.f;
+    __syncthreads();
+    if (i < m) out[i] = x;
+    __syncthreads();
+  }
+}
+
+constexpr int kMoveThreads = 256;
+// Destination slots per CTA and pass.
+constexpr int kMoveSlots = 64, kMoveSlotsInPlace = 256;
+
+// Kept keys and values of one (row, layer, kv head) to their destination slots.  Out of
+// place, blockIdx.x numbers (item, 64 destination slots).  IN_PLACE: one CTA walks all of
+// an item's slots from the first that moves, 256 at a time with a barrier between a pass's
+// loads and its stores -- a source slot never lies below its destination, so what a pass
+// overwrites has been read; blockIdx.z takes one of four quarters of the head dimension.
+template <int D, bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kChunks = IN_PLACE ? D / 32 : D / 8;  // 16-byte chunks of a slot per CTA
+  constexpr int kSlots = IN_PLACE ? kMoveSlotsInPlace : kMoveSlots;
+  constexpr int kUnits = kSlots * kChunks / kMoveThreads;
+  static_assert(kUnits >= 1, "every thread has a chunk");
+  const int passes = (p.keep + kSlots - 1) / kSlots;
+  const EvictItem &it = p.items[IN_PLACE ? blockIdx.x : blockIdx.x / passes];
+  const int g = blockIdx.y;
+  const int m = min(it.slots, p.keep);
+  const int32_t *kept = it.kept + (int64_t)g * p.keep;
+  const int chunk0 = IN_PLACE ? blockIdx.z * kChunks : 0;
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  int i0 = IN_PLACE ? 0 : (blockIdx.x % passes) * kSlots;
+  if (i0 >= m) return;
+  if (IN_PLACE) {  // kept[i] - i never falls: the first slot that moves
+    int lo = 0, hi = m;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (kept[mid] > mid) hi = mid;
+      else lo = mid + 1;
+    }
+    i0 = lo;
+  }
+  for (; i0 < m; i0 += kSlots) {
+    uint4 k[kUnits], v[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int x = threadIdx.x + u * kMoveThreads, i = i0 + x / kChunks;
+      if (i >= m) continue;
+      const int64_t s = kv_row(p.src_pt, it.src_row, p.Hk, g, p.src_seg, kept[i]) * D +
+                        8 * (chunk0 + x % kChunks);
+      k[u] = *reinterpret_cast<const uint4 *>(it.src_k + s);
+      v[u] = *reinterpret_cast<const uint4 *>(it.src_v + s);
+    }
+    if (IN_PLACE) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int x = threadIdx.x + u * kMoveThreads, i = i0 + x / kChunks;
+      if (i >= m) continue;
+      const int64_t d = kv_row(p.dst_pt, it.dst_row, p.Hk, g, p.dst_seg, i) * D +
+                        8 * (chunk0 + x % kChunks);
+      *reinterpret_cast<uint4 *>(it.dst_k + d) = k[u];
+      *reinterpret_cast<uint4 *>(it.dst_v + d) = v[u];
+    }
+    if (!IN_PLACE) return;
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s, bool pdl) {
+  if (p.n_items <= 0) return cudaSuccess;
+  const dim3 grid(p.n_items, p.Hk);
+  if (p.max_slots <= kHeld)
+    return launch_k(evict_select_kernel<true>, grid, dim3(kThreads), 4 * (size_t)p.max_slots, s, p,
+                    pdl);
+  return launch_k(evict_select_kernel<false>, grid, dim3(kThreads), 0, s, p, pdl);
+}
+
+cudaError_t launch_evict_move(const EvictParams &p, bool in_place, cudaStream_t s, bool pdl) {
+  if (p.n_items <= 0) return cudaSuccess;
+  const dim3 block(kMoveThreads);
+  if (in_place) {
+    const dim3 grid(p.n_items, p.Hk, 4);
+    return p.D == 128 ? launch_k(evict_move_kernel<128, true>, grid, block, 0, s, p, pdl)
+                      : launch_k(evict_move_kernel<64, true>, grid, block, 0, s, p, pdl);
+  }
+  const dim3 grid(p.n_items * ((p.keep + kMoveSlots - 1) / kMoveSlots), p.Hk);
+  return p.D == 128 ? launch_k(evict_move_kernel<128, false>, grid, block, 0, s, p, pdl)
+                    : launch_k(evict_move_kernel<64, false>, grid, block, 0, s, p, pdl);
+}
+
+cudaError_t configure_evict() {
+  return cudaFuncSetAttribute(evict_select_kernel<true>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kHeld);
+}
+
+}  // namespace kvinc

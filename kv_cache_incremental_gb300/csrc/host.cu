@@ -23,6 +23,7 @@ cudaError_t configure_decode();
 cudaError_t configure_prefill();
 cudaError_t configure_prefill_tc();
 cudaError_t configure_select();
+cudaError_t configure_evict();
 cudaError_t launch_prefill_tc(const PrefillParams &p, int D, int tiles, cudaStream_t s,
                               bool pdl);
 int prefill_tc_tiles(int D, int n_rho);
@@ -113,6 +114,9 @@ struct kv_cache {
   double theta;
   std::vector<int32_t> kind;
   std::vector<int32_t> lens;  // host mirror
+  // positions of each row that the full-length caches no longer hold (kv_evict_rows): the
+  // row fills slots [0, lens - dropped), its next token goes to slot lens - dropped
+  std::vector<int32_t> dropped;
   std::vector<void *> K, V;
   std::vector<int> seg_rows;
   std::vector<CUtensorMap> tmK, tmV;
@@ -202,6 +206,13 @@ PageTable page_table(const kv_cache *c, int layer) {
   pt.max_blocks = paged_layer(c, layer) ? c->max_blocks : 0;
   pt.n_pool = c->n_blocks;
   return pt;
+}
+
+// Keys a row holds in the full-length caches, and where token 0 of a call goes on a layer: a
+// slot of a cache, a position on a sliding layer (hybrid caches evict nothing).
+int slots_of(const kv_cache *c, int row) { return c->lens[row] - c->dropped[row]; }
+int start_of(const kv_cache *c, int layer, int row) {
+  return cache_layer(c, layer) ? slots_of(c, row) : c->lens[row];
 }
 
 int blocks_for(int len) { return (len + kBlockTokens - 1) / kBlockTokens; }
@@ -327,6 +338,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 struct DecodeIn {
   int cache_row, call_row, pos;
+  int slot;  // of the new key in a full-length cache
 };
 
 // What the split planners read of a layer: the device's SM count and the layer's shape
@@ -443,7 +455,7 @@ void plan_decode(const Geom &g, const std::vector<DecodeIn> &in, DecodeParams &p
     r.cache_row = in[i].cache_row;
     r.call_row = (uint16_t)in[i].call_row;
     r.pos = in[i].pos;
-    r.nk = sliding ? std::min(in[i].pos + 1, g.R) : in[i].pos + 1;
+    r.nk = sliding ? std::min(in[i].pos + 1, g.R) : in[i].slot + 1;
     r.ctr = in[i].cache_row;
     if (hybrid) nk2[i] = std::min(in[i].pos + 1, g.R);
     kv_bytes += 2.0 * (r.nk + nk2[i]) * g.Hk * g.D * 2.0;
@@ -673,14 +685,15 @@ int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfl
     std::vector<PrefillRow> rows;
     for (int i = 0; i < Bs; ++i)
       if (n_new[i] >= 2 && n_new[i] > off)
-        rows.push_back({cache_rows[i], i, c->lens[cache_rows[i]] + off,
-                        std::min(kChunk, n_new[i] - off), 0});
+        rows.push_back({cache_rows[i], i, start_of(c, layer, cache_rows[i]) + off,
+                        std::min(kChunk, n_new[i] - off), 0, 0, 0, 0,
+                        c->lens[cache_rows[i]] - start_of(c, layer, cache_rows[i])});
     return rows;
   };
   if (c->n_blocks > 0) {  // pool blocks for the new positions, before anything is enqueued
     std::vector<std::pair<int, int>> want;
     for (int i = 0; i < Bs; ++i)
-      if (n_new[i] > 0) want.push_back({cache_rows[i], c->lens[cache_rows[i]] + n_new[i]});
+      if (n_new[i] > 0) want.push_back({cache_rows[i], slots_of(c, cache_rows[i]) + n_new[i]});
     const int rc = ensure_blocks(c, want, s);
     if (rc != KV_OK) return rc;
   }
@@ -697,12 +710,13 @@ int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfl
     const std::vector<PrefillRow> prows = chunk_rows(off);
     if (off == 0)
       for (int i = 0; i < Bs; ++i)
-        if (n_new[i] == 1) drows.push_back({cache_rows[i], i, c->lens[cache_rows[i]]});
+        if (n_new[i] == 1)
+          drows.push_back({cache_rows[i], i, c->lens[cache_rows[i]], slots_of(c, cache_rows[i])});
     for (const PrefillRow &r : prows) {
       if (writes_global)
         arows.push_back({r.cache_row, r.call_row, r.lens, r.n,
-                         sliding ? kDestScratch : kDestGlobal, 0});
-      if (hybrid) lrows.push_back({r.cache_row, r.call_row, r.lens, r.n, kDestScratch, 0});
+                         sliding ? kDestScratch : kDestGlobal, 0, r.shift});
+      if (hybrid) lrows.push_back({r.cache_row, r.call_row, r.lens, r.n, kDestScratch, 0, 0});
     }
 
     // ---- RoPE + append of the chunk rows of this sub-chunk (a hybrid layer: the global
@@ -942,7 +956,8 @@ static int create_impl(kv_cache **out, int B, int max_len, int Hq, int Hk, int D
   DeviceGuard guard(device);
   if (!get_encode_fn()) return KV_ERR_CUDA;
   if (configure_decode() != cudaSuccess || configure_prefill() != cudaSuccess ||
-      configure_prefill_tc() != cudaSuccess || configure_select() != cudaSuccess)
+      configure_prefill_tc() != cudaSuccess || configure_select() != cudaSuccess ||
+      configure_evict() != cudaSuccess)
     return KV_ERR_CUDA;
 
   kv_cache *c = new kv_cache();
@@ -958,6 +973,7 @@ static int create_impl(kv_cache **out, int B, int max_len, int Hq, int Hk, int D
   c->theta = rope_theta;
   c->kind.assign(layer_kind, layer_kind + n_layers);
   c->lens.assign(B, 0);
+  c->dropped.assign(B, 0);
   cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, device);
   if (c->num_sms < 1) c->num_sms = 1;
 
@@ -1151,7 +1167,7 @@ int kv_reset(kv_cache *c, const int32_t *rows, int n_rows, void *stream) {
   const int rc = state_update(c, rv, nullptr, true, (cudaStream_t)stream);
   if (rc != KV_OK) return rc;
   for (int r : rv) {
-    c->lens[r] = 0;
+    c->lens[r] = c->dropped[r] = 0;
     release_blocks(c, r, 0);  // later launches on this stream may reuse them
     trim_bounds(c, r, 0);
     for (auto &he : c->hy_end)
@@ -1429,7 +1445,7 @@ int kv_plan_decode(int num_sms, int Hq, int Hk, int D, int R, int kind, int n_ro
   std::vector<DecodeIn> in(n_rows);
   for (int i = 0; i < n_rows; ++i) {
     if (pos[i] < 0 || pos[i] >= kPlanMaxLen) return KV_ERR_ARG;
-    in[i] = {i, i, pos[i]};
+    in[i] = {i, i, pos[i], pos[i]};
   }
   const Geom g{num_sms, Hq, Hk, D, kind == KV_GLOBAL ? 0 : R, kind};
   std::unique_ptr<DecodeParams> p(new DecodeParams());
@@ -1460,7 +1476,7 @@ int kv_plan_prefill(int num_sms, int Hq, int Hk, int D, int R, int kind, int n_r
   for (int i = 0; i < n_rows; ++i) {
     if (lens[i] < 0 || n[i] < 1 || n[i] > kChunk || lens[i] > kPlanMaxLen - n[i])
       return KV_ERR_ARG;
-    prows[i] = {i, i, lens[i], n[i], 0, 0, 0, 0};
+    prows[i] = {i, i, lens[i], n[i], 0, 0, 0, 0, 0};
   }
   const Geom g{num_sms, Hq, Hk, D, kind == KV_GLOBAL ? 0 : R, kind};
   std::vector<PrefillRow> ents[kPrefillKinds];
@@ -1566,7 +1582,8 @@ void plan_step(kv_step_graph *g) {
   kv_cache *c = g->c;
   std::vector<DecodeIn> batch(g->Bs);
   for (int i = 0; i < g->Bs; ++i)
-    batch[i] = {g->rows[i], i, std::min(c->lens[g->rows[i]], c->max_len - 1)};
+    batch[i] = {g->rows[i], i, std::min(c->lens[g->rows[i]], c->max_len - 1),
+                std::min(c->lens[g->rows[i]], c->max_len - 1) - c->dropped[g->rows[i]]};
   const int64_t q_row = (int64_t)c->Hq * c->D, kv_row = (int64_t)c->Hk * c->D;
   g->bytes = 0;
   g->flops = 0;
@@ -1752,7 +1769,7 @@ int kv_step_graph_launch(kv_step_graph *g, void *stream) {
   cudaStream_t s = (cudaStream_t)stream;
   if (c->n_blocks > 0) {  // the new position's block, written to the table before the replay
     std::vector<std::pair<int, int>> want;
-    for (int r : g->rows) want.push_back({r, c->lens[r] + 1});
+    for (int r : g->rows) want.push_back({r, slots_of(c, r) + 1});
     const int rc = ensure_blocks(c, want, s);
     if (rc != KV_OK) return rc;
   }
@@ -1949,6 +1966,7 @@ int kv_copy_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
     if (d < 0 || d >= dst->B || r < 0 || r >= src->B || dseen[d]) return KV_ERR_ARG;
     dseen[d] = 1;
     kp[i] = keep ? keep[i] : src->lens[r];
+    if (src->dropped[r] > 0) return KV_ERR_ARG;  // its slots are not its first positions
     if (kp[i] < 0 || kp[i] > dst->max_len || !positions_present(src, src->lens[r], kp[i], dst->R))
       return KV_ERR_ARG;
   }
@@ -2072,6 +2090,7 @@ int kv_copy_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
   if (set_ring_state(dst, rows, kp, s) != KV_OK) return KV_ERR_CUDA;
   for (int i = 0; i < n; ++i) {
     dst->lens[dst_rows[i]] = kp[i];
+    dst->dropped[dst_rows[i]] = 0;
     release_blocks(dst, dst_rows[i], kp[i]);  // a shortened row gives its tail back
     trim_bounds(dst, dst_rows[i], in_place(i) ? kp[i] : 0);
     for (auto &he : dst->hy_end)
@@ -2156,7 +2175,8 @@ static int export_import(kv_cache *c, int row, int keep, void *buf, int64_t byte
 
 int kv_export_row(const kv_cache *c, int row, int keep, void *dst, int64_t bytes, void *stream) {
   if (!c || row < 0 || row >= c->B || !dst || (reinterpret_cast<uintptr_t>(dst) & 15u)) return KV_ERR_ARG;
-  if (keep < 0 || !positions_present(c, c->lens[row], keep, c->R)) return KV_ERR_ARG;
+  if (keep < 0 || c->dropped[row] > 0 || !positions_present(c, c->lens[row], keep, c->R))
+    return KV_ERR_ARG;
   if (bytes != kv_export_bytes(c, keep)) return KV_ERR_ARG;
   DeviceGuard guard(c->device);
   return export_import(const_cast<kv_cache *>(c), row, keep, dst, bytes, (cudaStream_t)stream,
@@ -2180,6 +2200,7 @@ int kv_import_row(kv_cache *c, int row, int keep, const void *src, int64_t bytes
   if (rc != KV_OK) return rc;
   if (set_ring_state(c, {row}, {keep}, s) != KV_OK) return KV_ERR_CUDA;
   c->lens[row] = keep;
+  c->dropped[row] = 0;
   release_blocks(c, row, keep);
   trim_bounds(c, row, 0);
   for (auto &he : c->hy_end)
@@ -2365,7 +2386,7 @@ int kv_sparse_update(kv_cache *c, int layer, const int32_t *rows, int n_rows, vo
     if (r < 0 || r >= c->B || seen[r]) return KV_ERR_ARG;
     seen[r] = 1;
     rv.push_back(r);
-    slots.push_back(c->lens[r]);
+    slots.push_back(slots_of(c, r));
   }
   DeviceGuard guard(c->device);
   c->cur_layer = layer;
@@ -2397,10 +2418,10 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
   for (int i = 0; i < Bs; ++i) {
     if (n_new[i] == 0) continue;
     const int r = cache_rows[i];
-    want.push_back({r, c->lens[r] + n_new[i]});
+    want.push_back({r, slots_of(c, r) + n_new[i]});
     live.push_back(r);
-    slots.push_back(c->lens[r] + n_new[i]);
-    kept.push_back(c->lens[r]);
+    slots.push_back(slots_of(c, r) + n_new[i]);
+    kept.push_back(slots_of(c, r));
   }
   rc = ensure_blocks(c, want, s);  // before anything else is enqueued
   if (rc != KV_OK) return rc;
@@ -2408,8 +2429,9 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
     std::vector<AppendRow> arows;
     for (int i = 0; i < Bs; ++i)
       if (n_new[i] > off)
-        arows.push_back({cache_rows[i], i, c->lens[cache_rows[i]] + off,
-                         std::min(kChunk, n_new[i] - off), kDestGlobal, 0});
+        arows.push_back({cache_rows[i], i, slots_of(c, cache_rows[i]) + off,
+                         std::min(kChunk, n_new[i] - off), kDestGlobal, 0,
+                         c->dropped[cache_rows[i]]});
     rc = launch_append_rows(c, layer, (const __nv_bfloat16 *)k, (const __nv_bfloat16 *)v, C, off,
                             arows, s);
     if (rc != KV_OK) return rc;
@@ -2421,7 +2443,7 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
   std::vector<SelectQuery> batch;
   for (int i = 0; i < Bs; ++i)
     for (int t = 0; t < n_new[i]; ++t) {
-      const int pos = c->lens[cache_rows[i]] + t, tok = i * C + t;
+      const int tok = i * C + t;
       if (!batch.empty() &&
           ((int)batch.size() == kMaxRowsPerLaunch || tok - batch[0].tok > 0xffff)) {
         rc = attend_selected(c, layer, (const __nv_bfloat16 *)q, (__nv_bfloat16 *)out, batch, sink,
@@ -2429,10 +2451,366 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
         if (rc != KV_OK) return rc;
         batch.clear();
       }
-      batch.push_back({cache_rows[i], pos, pos, tok});
+      batch.push_back({cache_rows[i], slots_of(c, cache_rows[i]) + t,
+                       c->lens[cache_rows[i]] + t, tok});
     }
   return attend_selected(c, layer, (const __nv_bfloat16 *)q, (__nv_bfloat16 *)out, batch, sink,
                          top_k, recent, selected, s);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- attention weights
+namespace {
+
+// A row of an accumulating call: its tokens and the first counted one.
+struct WeightsIn {
+  int cache_row, call_row, n, t0;
+};
+
+// Tokens of a row whose query vectors are handled together.
+constexpr int kWeightGroup = kChunk;
+
+// acc_out = acc_in + the weights of the rows' counted tokens, whose keys are appended.
+// Tokens are taken in groups of at most kWeightGroup per row; the first group starts from
+// acc_in, the others add to acc_out.  Rows are batched so that pass 1's partials, one (m, l)
+// per query vector and key split, fit the prefill partials' reserve.
+int accumulate_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
+                       const std::vector<WeightsIn> &in, const float *acc_in, float *acc_out,
+                       cudaStream_t s) {
+  static thread_local WeightsParams p;
+  const int Hq = c->Hq, Hk = c->Hk, D = c->D, rep = Hq / Hk;
+  const int64_t cap = c->ppart_cap;
+  const int group = (int)std::min<int64_t>(kWeightGroup, cap / Hq);
+  p.K = (const __nv_bfloat16 *)c->K[layer];
+  p.q = q;
+  p.q_row_stride = (int64_t)C * Hq * D;
+  p.rope = c->rope;
+  p.part_ml = c->ppart_ml;
+  p.acc_out = acc_out;
+  p.acc_stride = c->max_len;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rep = rep;
+  p.D = D;
+  p.seg_rows = c->seg_rows[layer];
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  p.pt = page_table(c, layer);
+  const auto tiles = [](int keys) { return (keys + kWeightTile - 1) / kWeightTile; };
+  // the launches' rows of one kind (see launch_weights): single tokens apart from chunks
+  for (int kind = 0; kind < 2; ++kind) {
+    int most = 0;
+    for (const WeightsIn &w : in)
+      if ((w.n - w.t0 == 1) == (kind == 0)) most = std::max(most, w.n - w.t0);
+    for (int g0 = 0; g0 < most; g0 += group) {
+      std::vector<WeightsRow> rows;
+      for (const WeightsIn &w : in) {
+        if ((w.n - w.t0 == 1) != (kind == 0) || w.n - w.t0 <= g0) continue;
+        WeightsRow r = {};
+        r.cache_row = w.cache_row;
+        r.call_row = w.call_row;
+        r.slots = slots_of(c, w.cache_row);
+        r.shift = c->dropped[w.cache_row];
+        r.n = w.n;
+        r.t0 = w.t0 + g0;
+        r.t1 = std::min(w.n, r.t0 + group);
+        r.first = g0 == 0 ? 1 : 0;
+        rows.push_back(r);
+      }
+      for (size_t r0 = 0; r0 < rows.size();) {
+        // as many rows as the partials hold at one split each
+        size_t r1 = r0;
+        int64_t vecs = 0, work = 0;
+        while (r1 < rows.size() && r1 - r0 < (size_t)kMaxRowsPerLaunch) {
+          const int64_t v = (int64_t)(rows[r1].t1 - rows[r1].t0) * Hq;
+          if (vecs + v > cap) break;
+          vecs += v;
+          work += tiles(rows[r1].slots + rows[r1].t1);
+          ++r1;
+        }
+        // pass 1: about four CTAs per SM in all, splits of at least four tiles, longer until
+        // the partials fit
+        int64_t per = std::max<int64_t>(4, (work * Hk + 4 * c->num_sms - 1) / (4 * c->num_sms));
+        for (;; per *= 2) {
+          int64_t part = 0;
+          int item = 0, longest = 1;
+          for (size_t j = r0; j < r1; ++j) {
+            WeightsRow &r = p.rows[j - r0];
+            r = rows[j];
+            const int nt = tiles(r.slots + r.t1);
+            longest = std::max(longest, nt);
+            r.split_tiles = (int)std::min<int64_t>(per, nt);
+            r.n_splits = (nt + r.split_tiles - 1) / r.split_tiles;
+            r.item0 = item;
+            r.part = (int32_t)part;
+            item += r.n_splits;
+            part += (int64_t)r.n_splits * (r.t1 - r.t0) * Hq;
+          }
+          p.n_items = item;
+          if (part <= cap || per >= longest) break;
+        }
+        p.n_rows = (int)(r1 - r0);
+        double kb = 0, fl = 0;
+        for (int j = 0; j < p.n_rows; ++j) {
+          const WeightsRow &r = p.rows[j];
+          kb += 2.0 * (r.slots + r.t1) * Hk * D;
+          fl += 2.0 * (r.slots + r.t1) * (double)(r.t1 - r.t0) * Hq * D;
+        }
+        p.acc_in = g0 == 0 ? acc_in : acc_out;
+        cudaError_t e = timed(c, KV_KERNEL_WEIGHTS, kb, fl, s,
+                              [&] { return launch_weights(p, 1, s, c->pdl); });
+        if (e != cudaSuccess) return KV_ERR_CUDA;
+        // pass 2: a CTA per key tile of every slot that the call defines
+        int item = 0;
+        double ab = 0;
+        for (int j = 0; j < p.n_rows; ++j) {
+          WeightsRow &r = p.rows[j];
+          r.item0 = item;
+          item += tiles(r.slots + r.n);
+          ab += 8.0 * (r.slots + r.n) * Hk;
+        }
+        p.n_items = item;
+        e = timed(c, KV_KERNEL_WEIGHTS, kb + ab, fl, s,
+                  [&] { return launch_weights(p, 2, s, c->pdl); });
+        if (e != cudaSuccess) return KV_ERR_CUDA;
+        r0 = r1;
+      }
+    }
+  }
+  return KV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, const void *v, int Hq,
+                      int C, const int32_t *n_new, const int32_t *rows, int Bs, int last,
+                      const float *acc_in, float *acc_out, void *out, void *stream) {
+  if (!c || layer < 0 || layer >= c->n_layers || Hq != c->Hq || C < 1) return KV_ERR_ARG;
+  if (c->kind[layer] != KV_GLOBAL || last < 1) return KV_ERR_ARG;
+  std::vector<int32_t> cache_rows;
+  int rc = check_rows(c, n_new, rows, Bs, C, cache_rows);
+  if (rc != KV_OK) return rc;
+  std::vector<WeightsIn> in;
+  for (int i = 0; i < Bs; ++i)
+    if (n_new[i] > 0)
+      in.push_back({cache_rows[i], i, n_new[i], n_new[i] - std::min(n_new[i], last)});
+  if (in.empty()) return KV_OK;
+  if (!q || !k || !v || !out || !acc_in || !acc_out || !aligned16(q) || !aligned16(k) ||
+      !aligned16(v) || !aligned16(out) ||
+      ((reinterpret_cast<uintptr_t>(acc_in) | reinterpret_cast<uintptr_t>(acc_out)) & 3u))
+    return KV_ERR_ARG;
+  if (Hq > c->ppart_cap) return KV_ERR_SCRATCH;
+  DeviceGuard guard(c->device);
+  cudaStream_t s = (cudaStream_t)stream;
+  rc = append_device(c, layer, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)k,
+                     (const __nv_bfloat16 *)v, C, n_new, cache_rows, Bs, (__nv_bfloat16 *)out, s);
+  if (rc != KV_OK) return rc;
+  return accumulate_weights(c, layer, (const __nv_bfloat16 *)q, C, in, acc_in, acc_out, s);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- eviction
+extern "C" {
+
+int kv_get_slots(const kv_cache *c, int32_t *slots_out) {
+  if (!c || !slots_out) return KV_ERR_ARG;
+  for (int b = 0; b < c->B; ++b) slots_out[b] = slots_of(c, b);
+  return KV_OK;
+}
+
+int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
+                  const int32_t *src_rows, int n, int keep, int recent,
+                  const float *const *acc_in, float *const *acc_out, int32_t *const *kept,
+                  void *stream) {
+  if (!dst || !src || n < 0 || (n > 0 && (!dst_rows || !src_rows)) || keep < 1 || recent < 0 ||
+      recent > keep || !acc_in || !kept)
+    return KV_ERR_ARG;
+  if (!same_layout(dst, src) || has_hybrid(dst) || keep > src->max_len || keep > dst->max_len)
+    return KV_ERR_ARG;
+  std::vector<int> layers;
+  for (int l = 0; l < dst->n_layers; ++l) {
+    if (dst->kind[l] != KV_GLOBAL) continue;
+    layers.push_back(l);
+    if (!acc_in[l] || !kept[l] || (reinterpret_cast<uintptr_t>(acc_in[l]) & 3u) ||
+        (reinterpret_cast<uintptr_t>(kept[l]) & 3u) ||
+        (acc_out && (reinterpret_cast<uintptr_t>(acc_out[l]) & 3u)))
+      return KV_ERR_ARG;
+  }
+  if (layers.empty()) return KV_ERR_ARG;
+  std::vector<char> dseen(dst->B, 0);
+  for (int i = 0; i < n; ++i) {
+    const int d = dst_rows[i], r = src_rows[i];
+    if (d < 0 || d >= dst->B || r < 0 || r >= src->B || dseen[d]) return KV_ERR_ARG;
+    dseen[d] = 1;
+    const int len = src->lens[r];
+    if (len > dst->max_len || !positions_present(src, len, len, dst->R)) return KV_ERR_ARG;
+  }
+  if (dst == src)  // a row written by one pair must not be read by another
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < n; ++j)
+        if (i != j && dst_rows[i] == src_rows[j]) return KV_ERR_ARG;
+  if (n == 0) return KV_OK;
+  DeviceGuard guard(dst->device);
+  cudaStream_t s = (cudaStream_t)stream;
+  std::vector<int32_t> slots(n), m(n), lens(n);
+  const auto in_place = [&](int i) { return dst == src && dst_rows[i] == src_rows[i]; };
+  for (int i = 0; i < n; ++i) {
+    lens[i] = src->lens[src_rows[i]];
+    slots[i] = slots_of(src, src_rows[i]);
+    m[i] = std::min(slots[i], keep);
+  }
+  // Pool blocks, all or nothing before anything is enqueued.  A row cut in place keeps its
+  // first blocks, with copies of those that other rows hold too (the kept keys are moved
+  // into them), and lets go of the others when the keys have moved; any other destination
+  // row lets go of its blocks and takes fresh ones.
+  const bool paged = dst->n_blocks > 0;
+  if (paged) {
+    std::unordered_map<int32_t, int32_t> drops;
+    int64_t take = 0;
+    for (int i = 0; i < n; ++i) {
+      const auto &rb = dst->rblocks[dst_rows[i]];
+      if (in_place(i)) {
+        if (slots[i] <= keep) continue;
+        for (int x = 0; x < blocks_for(m[i]); ++x) take += dst->refs[rb[x]] > 1;
+      } else {
+        take += blocks_for(m[i]);
+        for (int b : rb) ++drops[b];
+      }
+    }
+    int64_t freed = 0;
+    for (const auto &e : drops) freed += dst->refs[e.first] == e.second;
+    if (take > (int64_t)dst->free_blocks.size() + freed) return KV_ERR_POOL;
+    static thread_local TableParams tp;
+    static thread_local CopyParams cp;
+    tp.table = dst->table;
+    tp.max_blocks = dst->max_blocks;
+    tp.n = 0;
+    cp.Hk = dst->Hk;
+    cp.D = dst->D;
+    cp.n_items = 0;
+    std::vector<std::pair<int, int>> want;
+    for (int i = 0; i < n; ++i)
+      if (!in_place(i)) {
+        release_blocks(dst, dst_rows[i], 0);
+        want.push_back({dst_rows[i], m[i]});
+      }
+    int rc = KV_OK;
+    for (int i = 0; i < n && rc == KV_OK; ++i) {
+      if (!in_place(i) || slots[i] <= keep) continue;
+      auto &rb = dst->rblocks[dst_rows[i]];
+      for (int x = 0; x < blocks_for(m[i]) && rc == KV_OK; ++x) {
+        if (dst->refs[rb[x]] == 1) continue;
+        const int old = rb[x], nb = take_block(dst);
+        drop_block(dst, old);  // still held by another row
+        rb[x] = nb;
+        for (int l : layers) {
+          const Unit u{l, false, false};
+          if (add_copy(cp, block_item(dst, u, old, nb, x * kBlockTokens, (x + 1) * kBlockTokens),
+                       s) != KV_OK)
+            return KV_ERR_CUDA;
+        }
+        rc = put_entry(dst, tp, dst_rows[i], x, nb, s);
+      }
+    }
+    if (rc == KV_OK && tp.n > 0) rc = launch_table(tp, s) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    if (rc == KV_OK && cp.n_items) rc = flush_copies(cp, s);
+    if (rc == KV_OK) rc = ensure_blocks(dst, want, s);
+    if (rc != KV_OK) return rc;
+  }
+  dst->cur_layer = -1;
+  static thread_local EvictParams p;
+  p.acc_in_stride = src->max_len;
+  p.acc_out_stride = dst->max_len;
+  p.Hk = dst->Hk;
+  p.D = dst->D;
+  p.keep = keep;
+  p.recent = recent;
+  p.src_pt = page_table(src, layers[0]);
+  p.dst_pt = page_table(dst, layers[0]);
+  p.src_seg = src->seg_rows[layers[0]];
+  p.dst_seg = dst->seg_rows[layers[0]];
+  // Launches of up to kMaxEvictItems (pair, layer) items: the choice for all of them, then
+  // the moves, rows in place and others apart.
+  for (int place = 0; place < 2; ++place) {
+    p.n_items = p.max_slots = 0;
+    double bytes = 0;
+    const auto flush = [&]() -> int {
+      if (p.n_items == 0) return KV_OK;
+      cudaError_t e = timed(dst, KV_KERNEL_EVICT, 0, 0, s,
+                            [&] { return launch_evict_select(p, s, dst->pdl); });
+      if (e == cudaSuccess)
+        e = timed(dst, KV_KERNEL_EVICT, bytes, 0, s,
+                  [&] { return launch_evict_move(p, place == 1, s, dst->pdl); });
+      p.n_items = p.max_slots = 0;
+      bytes = 0;
+      return set_err(e);
+    };
+    for (int i = 0; i < n; ++i) {
+      if (in_place(i) != (place == 1)) continue;
+      for (int l : layers) {
+        EvictItem &it = p.items[p.n_items++];
+        it.acc_in = acc_in[l] + (int64_t)src_rows[i] * src->Hk * src->max_len;
+        it.acc_out = acc_out && acc_out[l]
+                         ? acc_out[l] + (int64_t)dst_rows[i] * dst->Hk * dst->max_len
+                         : nullptr;
+        it.kept = kept[l] + (int64_t)i * dst->Hk * keep;
+        it.src_k = (const __nv_bfloat16 *)src->K[l];
+        it.src_v = (const __nv_bfloat16 *)src->V[l];
+        it.dst_k = (__nv_bfloat16 *)dst->K[l];
+        it.dst_v = (__nv_bfloat16 *)dst->V[l];
+        it.src_row = src_rows[i];
+        it.dst_row = dst_rows[i];
+        it.slots = slots[i];
+        it.in_place = place;
+        p.max_slots = std::max(p.max_slots, (int)slots[i]);
+        bytes += dst->Hk * (8.0 * m[i] * dst->D + 4.0 * slots[i] + 8.0 * m[i]);
+        if (p.n_items == kMaxEvictItems && flush() != KV_OK) return KV_ERR_CUDA;
+      }
+    }
+    if (flush() != KV_OK) return KV_ERR_CUDA;
+  }
+  // sliding layers of rows that are not cut in place: their rings, position by position
+  static thread_local CopyParams cp;
+  cp.Hk = dst->Hk;
+  cp.D = dst->D;
+  cp.n_items = 0;
+  std::vector<int32_t> moved, moved_lens;
+  for (int i = 0; i < n; ++i) {
+    if (in_place(i)) continue;
+    moved.push_back(dst_rows[i]);
+    moved_lens.push_back(lens[i]);
+    for (int l = 0; l < dst->n_layers; ++l) {
+      if (dst->kind[l] != KV_SLIDING) continue;
+      const Unit u{l, false, true};
+      CopyItem it;
+      __nv_bfloat16 *sk, *sv;
+      row_block(src, u, src_rows[i], sk, sv, it.src_head_stride, it.src_table, it.src_pool);
+      it.src_k = sk;
+      it.src_v = sv;
+      row_block(dst, u, dst_rows[i], it.dst_k, it.dst_v, it.dst_head_stride, it.dst_table,
+                it.dst_pool);
+      it.p0 = first_kept(dst, u, lens[i]);
+      it.p1 = lens[i];
+      it.src_ring = src->R;
+      it.dst_ring = dst->R;
+      it.src_base = it.dst_base = 0;
+      if (add_copy(cp, it, s) != KV_OK) return KV_ERR_CUDA;
+    }
+  }
+  if (cp.n_items && flush_copies(cp, s) != KV_OK) return KV_ERR_CUDA;
+  note_launch(dst, s, -1);  // the storage was written
+  if (set_ring_state(dst, moved, moved_lens, s) != KV_OK) return KV_ERR_CUDA;
+  for (int i = 0; i < n; ++i) {
+    const int d = dst_rows[i];
+    dst->lens[d] = lens[i];
+    dst->dropped[d] = lens[i] - m[i];
+    release_blocks(dst, d, m[i]);
+    if (!in_place(i) || slots[i] > keep) trim_bounds(dst, d, 0);
+  }
+  return KV_OK;
 }
 
 const char *kv_strerror(int code) {

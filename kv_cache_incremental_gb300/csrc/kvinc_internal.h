@@ -73,10 +73,11 @@ enum DestMode : int32_t {
 struct AppendRow {
   int32_t cache_row;
   int32_t call_row;
-  int32_t lens;   // position of token t = 0 of this sub-chunk
+  int32_t lens;   // slot of token t = 0 of this sub-chunk (a ring's: its position)
   int32_t n;      // real tokens in this sub-chunk
   int32_t mode;   // DestMode
   int32_t blk0;   // first token block (8 tokens each) of this row in the grid
+  int32_t shift;  // a token's position minus its slot (rows with evicted keys)
 };
 
 struct AppendParams {
@@ -183,11 +184,12 @@ struct DecodeParams {  // 64-byte aligned through its CUtensorMap members
 struct PrefillRow {
   int32_t cache_row;
   int32_t call_row;
-  int32_t lens;   // position of token 0 of the sub-chunk
+  int32_t lens;   // slot of token 0 of the sub-chunk (layers with a ring: its position)
   int32_t n;      // tokens of the sub-chunk
   int32_t cta0;   // first CTA (query tile) of this entry
   int32_t tile0, tile1;
   int32_t part;
+  int32_t shift;  // a token's position minus its slot (rows with evicted keys)
 };
 
 struct PrefillParams {  // 64-byte aligned through its CUtensorMap members
@@ -341,6 +343,63 @@ struct SelectParams {
   SelectQuery queries[kMaxRowsPerLaunch];
 };
 
+// ---------------------------------------------------------------- attention weights
+// Per key of a row, the softmax weights that the counted query tokens [t0, n) of a call
+// give it, summed over them and over the kv head's query heads.  Pass 1 finds every query
+// vector's softmax maximum and sum over the row's keys, in parts per key split; pass 2 sums
+// the weights per key.  Query vectors are numbered (t - t0) * rep + head.
+struct WeightsRow {
+  int32_t cache_row;
+  int32_t call_row;
+  int32_t slots;    // keys before the call; token t sits at slot slots + t
+  int32_t shift;    // a token's position minus its slot
+  int32_t n;        // tokens of the call, all appended
+  int32_t t0, t1;   // counted tokens
+  int32_t first;    // 1: acc_in holds the accumulator of slots below `slots`; 0: of all slots
+  int32_t item0;    // first CTA (key split / key tile) of this row in the launch
+  int32_t n_splits, split_tiles;  // of pass 1, in kWeightTile keys
+  int32_t part;     // first (m, l) vector of the row
+};
+constexpr int kWeightTile = 128;  // keys per CTA and pass
+struct WeightsParams {
+  const __nv_bfloat16 *K;  // layer storage
+  const __nv_bfloat16 *q;  // [Bs][C][Hq][D]
+  int64_t q_row_stride;
+  const float2 *rope;
+  float2 *part_ml;         // [part + (split * Hk + g) * n_vec + vec]: max (log2 units), sum
+  const float *acc_in;     // [B][Hk][acc_stride]
+  float *acc_out;
+  int acc_stride;
+  int Hq, Hk, rep, D, seg_rows;
+  float scale_log2;
+  PageTable pt;
+  int n_rows, n_items;
+  WeightsRow rows[kMaxRowsPerLaunch];
+};
+
+// ---------------------------------------------------------------- eviction
+// One (row pair, global layer) of an eviction.
+struct EvictItem {
+  const float *acc_in;   // the source row's accumulator [Hk][acc_in_stride]
+  float *acc_out;        // the destination row's, or nullptr
+  int32_t *kept;         // [Hk][keep]
+  const __nv_bfloat16 *src_k, *src_v;  // layer storages (whole)
+  __nv_bfloat16 *dst_k, *dst_v;
+  int32_t src_row, dst_row;
+  int32_t slots;         // the source row's keys
+  int32_t in_place;      // the destination is the source row itself
+};
+constexpr int kMaxEvictItems = 256;
+struct EvictParams {
+  int acc_in_stride, acc_out_stride;
+  int Hk, D, keep, recent;
+  int src_seg, dst_seg;
+  int max_slots;          // most keys of a source row of the launch
+  PageTable src_pt, dst_pt;
+  int n_items;
+  EvictItem items[kMaxEvictItems];
+};
+
 // ---------------------------------------------------------------- launchers
 // Launch kernel(p) on s.  With pdl, as a programmatic dependent launch: the grid may start
 // while the previous kernel on the stream finishes, and waits for it (griddepcontrol.wait)
@@ -395,6 +454,10 @@ cudaError_t launch_commit(const CommitParams &p, cudaStream_t s, bool pdl = fals
 cudaError_t launch_state(const StateParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_bounds(const BoundsParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_select(const SelectParams &p, cudaStream_t s, bool pdl = false);
+cudaError_t launch_weights(const WeightsParams &p, int pass, cudaStream_t s, bool pdl = false);
+cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s, bool pdl = false);
+cudaError_t launch_evict_move(const EvictParams &p, bool in_place, cudaStream_t s,
+                              bool pdl = false);
 cudaError_t launch_wait_probe(int32_t *err, uint32_t limit, cudaStream_t s);
 // Opt kernels into their dynamic shared memory sizes (once per process and device).
 cudaError_t configure_kernels();
@@ -410,6 +473,8 @@ static_assert(sizeof(TableParams) <= kMaxParamBytes, "table parameters too large
 static_assert(sizeof(StateParams) <= kMaxParamBytes, "state parameters too large");
 static_assert(sizeof(BoundsParams) <= kMaxParamBytes, "bounds parameters too large");
 static_assert(sizeof(SelectParams) <= kMaxParamBytes, "select parameters too large");
+static_assert(sizeof(WeightsParams) <= kMaxParamBytes, "weights parameters too large");
+static_assert(sizeof(EvictParams) <= kMaxParamBytes, "eviction parameters too large");
 static_assert(sizeof(MergeParams) <= kMaxParamBytes, "merge parameters too large");
 
 }  // namespace kvinc

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) prefill_kernel(const __grid_constant
         const __nv_bfloat16 *x2 = reinterpret_cast<const __nv_bfloat16 *>(&x2v);
         __nv_bfloat16 *o1 = reinterpret_cast<__nv_bfloat16 *>(&lo);
         __nv_bfloat16 *o2 = reinterpret_cast<__nv_bfloat16 *>(&hi);
-        const float2 *cs = p.rope + (int64_t)(lens + t) * kHalf + 8 * c;
+        const float2 *cs = p.rope + (int64_t)(lens + row.shift + t) * kHalf + 8 * c;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float a = __bfloat162float(x1[j]), b = __bfloat162float(x2[j]);

@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(Roles<TQ>::kThreads, TQ == 1 ? 2 : 1)
       const int t = valid ? rho / p.rep : 0, h = valid ? rho % p.rep : 0;
       const __nv_bfloat16 *q = p.q + (int64_t)row.call_row * p.q_row_stride +
                                ((int64_t)t * p.Hq + g * p.rep + h) * D;
-      const float2 *cs = p.rope + (int64_t)(lens + t) * kHalf;
+      const float2 *cs = p.rope + (int64_t)(lens + row.shift + t) * kHalf;
       uint8_t *qtile = qsm + qt_me * Cfg::kQBytes;
 #pragma unroll 2
       for (int c = 0; c < kHalf / 8; ++c) {

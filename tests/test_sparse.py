@@ -46,7 +46,7 @@ def check(r, layer, rows, n_new, q, k, v, sink, top_k, recent, got, chosen):
         qr = f32(r.rotated(q[i, :n], L)).reshape(n, r.Hk, r.rep, r.D)
         Kf, Vf = f32(K), f32(V).astype(np.float64)
         for t in range(n):
-            slot = L + t
+            slot = K.shape[1] - n + t      # L + t unless keys were evicted
             for g in range(r.Hk):
                 want = choose(Kf[g], qr[t, g], slot, sink, top_k, recent)
                 mine = chosen[i, t, g]
