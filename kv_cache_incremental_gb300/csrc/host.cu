@@ -1927,8 +1927,9 @@ int put_entry(kv_cache *c, TableParams &tp, int row, int idx, int blk, cudaStrea
   if (++tp.n < kMaxTableEntries) return KV_OK;
   c->last_stream = s;
   c->last_kind = -1;
+  const cudaError_t e = launch_table(tp, s);
   tp.n = 0;
-  return launch_table(tp, s) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
 // Copy item for positions [p0, p1) of one pool block to another (paged unit u): both
