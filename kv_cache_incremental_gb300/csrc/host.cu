@@ -359,12 +359,13 @@ int storage_id(const kv_cache *c, int layer) {
 
 // Whether a decode launch of `layer` on `s` may stream K/V before its grid dependency
 // wait: the cache's previous launch on s wrote nothing it reads -- a decode of another
-// storage (new keys, partials, tickets, outputs) or a ring-state update (lpos only).
+// storage (new keys, partials, tickets, outputs), a ring-state update (lpos only) or the
+// last launch of a weight accumulation (the caller's accumulator only).
 // Launches of the caller between them write no cache storage; older grids have completed
 // by the time a programmatic launch starts.
 bool early_kv_ok(const kv_cache *c, int layer, cudaStream_t s) {
   if (!c->pdl || c->last_stream != s) return false;
-  if (c->last_kind == KV_KERNEL_STATE) return true;
+  if (c->last_kind == KV_KERNEL_STATE || c->last_kind == KV_KERNEL_WEIGHTS) return true;
   return c->last_kind == KV_KERNEL_DECODE && c->last_layer >= 0 &&
          storage_id(c, c->last_layer) != storage_id(c, layer);
 }
@@ -506,6 +507,7 @@ void fill_decode(const kv_cache *c, int layer, const __nv_bfloat16 *q, const __n
   dp.fuse_append2 = hybrid ? 1 : 0;
   dp.early_kv = 0;
   dp.list = nullptr;
+  dp.scores = nullptr;
   dp.tmap_k2 = hybrid ? c->tmRK[layer] : c->tmK[layer];
   dp.tmap_v2 = hybrid ? c->tmRV[layer] : c->tmV[layer];
   dp.k_new2 = k_local;
@@ -2324,6 +2326,7 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat1
   dp.early_kv = 0;
   dp.list = sp.list;
   dp.list_stride = sp.max_select;
+  dp.scores = nullptr;
   static const int no_ring[kMaxRowsPerLaunch] = {};
   // the partials are the cache's own: kMaxSplits slots for each of up to min(B, 512) rows
   plan_decode_splits(c->num_sms, Hk, n, no_ring, dp, std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
@@ -2581,6 +2584,64 @@ int accumulate_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
   return KV_OK;
 }
 
+// Append, attention and weights of single-token rows in one pass over their keys: decode
+// launches that store the scores in the prefill partials' reserve, each followed by the
+// join.  `in` holds the rows whose scores fit; a launch takes as many as fit together, all
+// launches about equally many.
+int decode_with_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
+                        const __nv_bfloat16 *v, int C, const std::vector<WeightsIn> &in,
+                        const float *acc_in, float *acc_out, __nv_bfloat16 *out,
+                        cudaStream_t s) {
+  static thread_local DecodeParams dp;
+  static thread_local JoinParams jp;
+  int longest = 0;
+  for (const WeightsIn &w : in) longest = std::max(longest, slots_of(c, w.cache_row) + 1);
+  const int64_t stride = (longest + 3) / 4 * 4;
+  const int64_t room = c->ppart_cap * c->D / (c->Hq * stride);
+  const size_t most = (size_t)std::min<int64_t>(
+      std::min<int64_t>(room, c->ppart_cap / c->Hq), kMaxRowsPerLaunch);
+  const size_t launches = (in.size() + most - 1) / most;
+  const size_t per = (in.size() + launches - 1) / launches;
+  for (size_t r0 = 0; r0 < in.size(); r0 += per) {
+    const size_t r1 = std::min(in.size(), r0 + per);
+    std::vector<DecodeIn> batch;
+    jp.n_items = 0;
+    double ab = 0;
+    for (size_t j = r0; j < r1; ++j) {
+      const int r = in[j].cache_row, slot = slots_of(c, r);
+      batch.push_back({r, in[j].call_row, c->lens[r], slot});
+      jp.rows[j - r0] = {r, slot + 1, jp.n_items};
+      jp.n_items += (slot + kJoinSlots) / kJoinSlots;
+      ab += (slot + 1.0) * (8.0 * c->Hk + 4.0 * c->Hq);
+    }
+    double bytes = 0, fl = 0;
+    fill_decode(c, layer, q, k, v, out, (int64_t)C * c->Hq * c->D, (int64_t)C * c->Hk * c->D,
+                batch, dp, bytes, fl);
+    dp.scores = c->ppart_o;
+    dp.row_ml = c->ppart_ml;
+    dp.score_stride = stride;
+    dp.early_kv = early_kv_ok(c, layer, s) ? 1 : 0;
+    if (!c->pdl) dp.deep_pipeline = 0;
+    cudaError_t e = timed(c, KV_KERNEL_DECODE, bytes, fl, s, [&] {
+      return launch_decode(dp, c->D, c->Hq / c->Hk <= 8 ? 1 : 2, s, c->pdl);
+    });
+    if (e != cudaSuccess) return KV_ERR_CUDA;
+    jp.scores = c->ppart_o;
+    jp.row_ml = c->ppart_ml;
+    jp.score_stride = stride;
+    jp.acc_in = acc_in;
+    jp.acc_out = acc_out;
+    jp.acc_stride = c->max_len;
+    jp.Hq = c->Hq;
+    jp.Hk = c->Hk;
+    jp.rep = c->Hq / c->Hk;
+    jp.n_rows = (int)(r1 - r0);
+    e = timed(c, KV_KERNEL_WEIGHTS, ab, 0, s, [&] { return launch_join(jp, s, c->pdl); });
+    if (e != cudaSuccess) return KV_ERR_CUDA;
+  }
+  return KV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -2593,11 +2654,24 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
   std::vector<int32_t> cache_rows;
   int rc = check_rows(c, n_new, rows, Bs, C, cache_rows);
   if (rc != KV_OK) return rc;
-  std::vector<WeightsIn> in;
-  for (int i = 0; i < Bs; ++i)
-    if (n_new[i] > 0)
-      in.push_back({cache_rows[i], i, n_new[i], n_new[i] - std::min(n_new[i], last)});
-  if (in.empty()) return KV_OK;
+  // Single-token rows take one pass over their keys while a row's scores fit the reserve; the
+  // rest take their attention as kv_append gives it and then two passes over K.
+  std::vector<WeightsIn> single, in;
+  std::vector<int32_t> n_rest(n_new, n_new + std::max(Bs, 0));
+  std::vector<std::pair<int, int>> want;
+  for (int i = 0; i < Bs; ++i) {
+    if (n_new[i] == 0) continue;
+    const WeightsIn w = {cache_rows[i], i, n_new[i], n_new[i] - std::min(n_new[i], last)};
+    const int64_t stride = (slots_of(c, cache_rows[i]) + 1 + 3) / 4 * 4;
+    want.push_back({cache_rows[i], slots_of(c, cache_rows[i]) + n_new[i]});
+    if (n_new[i] == 1 && stride * c->Hq <= c->ppart_cap * c->D && c->Hq <= c->ppart_cap) {
+      single.push_back(w);
+      n_rest[i] = 0;
+    } else {
+      in.push_back(w);
+    }
+  }
+  if (want.empty()) return KV_OK;
   if (!q || !k || !v || !out || !acc_in || !acc_out || !aligned16(q) || !aligned16(k) ||
       !aligned16(v) || !aligned16(out) ||
       ((reinterpret_cast<uintptr_t>(acc_in) | reinterpret_cast<uintptr_t>(acc_out)) & 3u))
@@ -2605,8 +2679,19 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
   if (Hq > c->ppart_cap) return KV_ERR_SCRATCH;
   DeviceGuard guard(c->device);
   cudaStream_t s = (cudaStream_t)stream;
+  rc = ensure_blocks(c, want, s);  // every row's, before anything else is enqueued
+  if (rc != KV_OK) return rc;
+  c->cur_layer = layer;
+  if (!single.empty()) {
+    rc = decode_with_weights(c, layer, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)k,
+                             (const __nv_bfloat16 *)v, C, single, acc_in, acc_out,
+                             (__nv_bfloat16 *)out, s);
+    if (rc != KV_OK) return rc;
+  }
+  if (in.empty()) return KV_OK;
   rc = append_device(c, layer, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)k,
-                     (const __nv_bfloat16 *)v, C, n_new, cache_rows, Bs, (__nv_bfloat16 *)out, s);
+                     (const __nv_bfloat16 *)v, C, n_rest.data(), cache_rows, Bs,
+                     (__nv_bfloat16 *)out, s);
   if (rc != KV_OK) return rc;
   return accumulate_weights(c, layer, (const __nv_bfloat16 *)q, C, in, acc_in, acc_out, s);
 }

@@ -172,6 +172,12 @@ struct DecodeParams {  // 64-byte aligned through its CUtensorMap members
   // filled.  nullptr: tile t is slots [64 t, 64 t + 64).
   const int32_t *list;
   int list_stride;
+  // Accumulated weights (the scores variant): head hq's score of slot j, in log2 units, goes
+  // to scores[(r * Hq + hq) * score_stride + j] for row r of the launch, and the softmax
+  // maximum and the reciprocal of its sum to row_ml[r * Hq + hq].  nullptr: neither.
+  float *scores;
+  float2 *row_ml;
+  int64_t score_stride;
   DecodeRow rows[kMaxRowsPerLaunch];
 };
 
@@ -377,6 +383,26 @@ struct WeightsParams {
   WeightsRow rows[kMaxRowsPerLaunch];
 };
 
+// Weights of single-token rows from the scores that the decode kernel stored: a row of the
+// launch has `keys` slots, the last of them its new token's.
+struct JoinRow {
+  int32_t cache_row;
+  int32_t keys;
+  int32_t item0;  // first CTA (kJoinSlots slots) of this row
+};
+constexpr int kJoinSlots = 1024;
+struct JoinParams {
+  const float *scores;     // [row of the launch][Hq][score_stride]
+  const float2 *row_ml;    // [row][Hq]
+  int64_t score_stride;
+  const float *acc_in;     // [B][Hk][acc_stride]
+  float *acc_out;
+  int acc_stride;
+  int Hq, Hk, rep;
+  int n_rows, n_items;
+  JoinRow rows[kMaxRowsPerLaunch];
+};
+
 // ---------------------------------------------------------------- eviction
 // One (row pair, global layer) of an eviction.
 struct EvictItem {
@@ -455,6 +481,7 @@ cudaError_t launch_state(const StateParams &p, cudaStream_t s, bool pdl = false)
 cudaError_t launch_bounds(const BoundsParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_select(const SelectParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_weights(const WeightsParams &p, int pass, cudaStream_t s, bool pdl = false);
+cudaError_t launch_join(const JoinParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_evict_move(const EvictParams &p, bool in_place, cudaStream_t s,
                               bool pdl = false);
@@ -474,6 +501,7 @@ static_assert(sizeof(StateParams) <= kMaxParamBytes, "state parameters too large
 static_assert(sizeof(BoundsParams) <= kMaxParamBytes, "bounds parameters too large");
 static_assert(sizeof(SelectParams) <= kMaxParamBytes, "select parameters too large");
 static_assert(sizeof(WeightsParams) <= kMaxParamBytes, "weights parameters too large");
+static_assert(sizeof(JoinParams) <= kMaxParamBytes, "join parameters too large");
 static_assert(sizeof(EvictParams) <= kMaxParamBytes, "eviction parameters too large");
 static_assert(sizeof(MergeParams) <= kMaxParamBytes, "merge parameters too large");
 

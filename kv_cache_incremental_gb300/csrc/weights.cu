@@ -4,8 +4,11 @@
 // s_t = slots + t) and the group's heads h,
 //   acc_out[j] = acc_in[j] + sum_t sum_h [j <= s_t] 2^(x_thj - m_th) / l_th,
 //   x_thj = log2(e) / sqrt(D) q_th . K_j,  m_th = max_j x_thj,  l_th = sum_j 2^(x_thj - m_th).
-// A weight needs its query's m and l over all keys first, so there are two passes over K:
-// the first leaves (m, l) per query vector and key split, the second joins the splits and
+// A weight needs its query's m and l over all keys first.  For rows with a single new token
+// the decode kernel stores the scores on its one pass over K and V (decode_kernel.cuh, the
+// scores mode) and the join kernel turns them into weights: 8 bytes of scores per key and
+// head, written and read, beside the 4 D bytes of a key and value.  For chunks, and for rows
+// whose scores outgrow the room reserved for them, there are two passes over K: the first leaves (m, l) per query vector and key split, the second joins the splits and
 // sums the weights per key.  Both form S^T = K Q^T with mma.sync (keys on M, query vectors
 // on N): a key's weights then lie in the lanes of one quad and its sum over the queries
 // stays in a register; a query's running (m, l) over its lane's keys stays in registers
@@ -246,6 +249,44 @@ __global__ void __launch_bounds__(kWThreads)
   }
 }
 
+// Single-token rows: the scores are there already.  One CTA per (row, 1024 slots, kv head),
+// coalesced over slots; a thread's loads of its four slots are independent.
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p) {
+  __shared__ float2 ml[kMaxRep];
+  int lo = 0, hi = p.n_rows - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.rows[mid].item0 <= (int)blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const JoinRow &row = p.rows[lo];
+  const int g = blockIdx.y;
+  const int s0 = ((int)blockIdx.x - row.item0) * kJoinSlots + threadIdx.x;
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if (threadIdx.x < p.rep) ml[threadIdx.x] = p.row_ml[(int64_t)lo * p.Hq + g * p.rep + threadIdx.x];
+  __syncthreads();
+  const float *sc = p.scores + ((int64_t)lo * p.Hq + g * p.rep) * p.score_stride + s0;
+  const int64_t at = ((int64_t)row.cache_row * p.Hk + g) * p.acc_stride + s0;
+  constexpr int kPer = kJoinSlots / 256;
+  float sum[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    sum[i] = s0 + 256 * i < row.keys - 1 ? p.acc_in[at + 256 * i] : 0.f;
+  for (int h = 0; h < p.rep; ++h) {
+    const float2 e = ml[h];
+    float x[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      x[i] = s0 + 256 * i < row.keys ? sc[h * p.score_stride + 256 * i] : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum[i] += exp2f(x[i] - e.x) * e.y;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (s0 + 256 * i < row.keys) p.acc_out[at + 256 * i] = sum[i];
+}
+
 template <int D, int QT>
 cudaError_t launch_weights_t(const WeightsParams &p, int pass, cudaStream_t s, bool pdl) {
   const dim3 grid(p.n_items, p.Hk), block(kWThreads);
@@ -254,6 +295,11 @@ cudaError_t launch_weights_t(const WeightsParams &p, int pass, cudaStream_t s, b
 }
 
 }  // namespace
+
+cudaError_t launch_join(const JoinParams &p, cudaStream_t s, bool pdl) {
+  if (p.n_items <= 0) return cudaSuccess;
+  return launch_k(join_kernel, dim3(p.n_items, p.Hk), dim3(256), 0, s, p, pdl);
+}
 
 // Rows of a launch are of one kind: at most 8 query vectors (single tokens of groups of up
 // to 8 heads) in one fragment, at most 16 in two, else chunks of 64.
