@@ -2255,8 +2255,10 @@ int update_bounds(kv_cache *c, int layer, const std::vector<int32_t> &rows,
 }
 
 // Selection and attention of up to kMaxRowsPerLaunch queries, tokens [tok0, tok0 + 2^16) of
-// the call's q and out [tok][Hq][D].
-int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat16 *out,
+// the call's q and out [tok][Hq][D].  k, v: the tokens' keys and values [tok][Hk][D] when the
+// selection appends them (the queries are single tokens of different rows), else nullptr.
+int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
+                    const __nv_bfloat16 *v, __nv_bfloat16 *out,
                     const std::vector<SelectQuery> &qs, int sink, int top_k, int recent,
                     int32_t *selected, cudaStream_t s) {
   kv_cache::Sparse &sp = c->sparse;
@@ -2268,6 +2270,12 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat1
   p.rope = c->rope;
   p.bound = sp.bound[layer];
   p.scale = sp.scale[layer];
+  p.k = k;
+  p.v = v;
+  p.cache_k = (__nv_bfloat16 *)c->K[layer];
+  p.cache_v = (__nv_bfloat16 *)c->V[layer];
+  p.seg_rows = c->seg_rows[layer];
+  p.pt = page_table(c, layer);
   p.list = sp.list;
   p.selected = selected;
   p.Hq = Hq;
@@ -2288,7 +2296,7 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat1
     const int nb = qs[i].slot / kSparseBlock + 1, n_sel = std::min(nb, per);
     const int cand = nb > per ? nb - sink - recent : 0;
     p.max_cand = std::max(p.max_cand, cand);
-    sel_bytes += (double)cand * Hk * (2.0 * D + 4.0);
+    sel_bytes += (double)cand * Hk * (2.0 * D + 4.0) + (k ? 8.0 * Hk * D : 0.0);
     DecodeRow &r = dp.rows[i];
     r.cache_row = qs[i].cache_row;
     r.call_row = (uint16_t)(qs[i].tok - tok0);
@@ -2429,37 +2437,59 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
   }
   rc = ensure_blocks(c, want, s);  // before anything else is enqueued
   if (rc != KV_OK) return rc;
-  for (int off = 0; off < max_n; off += kChunk) {
-    std::vector<AppendRow> arows;
-    for (int i = 0; i < Bs; ++i)
-      if (n_new[i] > off)
-        arows.push_back({cache_rows[i], i, slots_of(c, cache_rows[i]) + off,
-                         std::min(kChunk, n_new[i] - off), kDestGlobal, 0,
-                         c->dropped[cache_rows[i]]});
-    rc = launch_append_rows(c, layer, (const __nv_bfloat16 *)k, (const __nv_bfloat16 *)v, C, off,
-                            arows, s);
+  const __nv_bfloat16 *kb = (const __nv_bfloat16 *)k, *vb = (const __nv_bfloat16 *)v;
+  // Calls of single-token rows append (and bound a row's one or two pending blocks) in the
+  // selection's launch; the others, and rows behind by more blocks, in launches before it.
+  std::vector<int32_t> &valid = c->sparse.valid[layer];
+  const bool fused = max_n == 1;
+  if (fused) {
+    std::vector<int32_t> far, far_slots;
+    for (size_t i = 0; i < live.size(); ++i)
+      if (kept[i] / kSparseBlock - valid[live[i]] > 1) {
+        far.push_back(live[i]);
+        far_slots.push_back(kept[i]);
+      }
+    if (!far.empty() && (rc = update_bounds(c, layer, far, far_slots, far_slots, s)) != KV_OK)
+      return rc;
+  } else {
+    for (int off = 0; off < max_n; off += kChunk) {
+      std::vector<AppendRow> arows;
+      for (int i = 0; i < Bs; ++i)
+        if (n_new[i] > off)
+          arows.push_back({cache_rows[i], i, slots_of(c, cache_rows[i]) + off,
+                           std::min(kChunk, n_new[i] - off), kDestGlobal, 0,
+                           c->dropped[cache_rows[i]]});
+      rc = launch_append_rows(c, layer, kb, vb, C, off, arows, s);
+      if (rc != KV_OK) return rc;
+    }
+    rc = update_bounds(c, layer, live, slots, kept, s);
     if (rc != KV_OK) return rc;
   }
-  rc = update_bounds(c, layer, live, slots, kept, s);
-  if (rc != KV_OK) return rc;
   // queries in launches of at most kMaxRowsPerLaunch, whose tokens lie within 2^16 of the
   // first one's (the kernels' 16-bit token index)
   std::vector<SelectQuery> batch;
+  const auto flush = [&]() -> int {
+    return attend_selected(c, layer, (const __nv_bfloat16 *)q, fused ? kb : nullptr,
+                           fused ? vb : nullptr, (__nv_bfloat16 *)out, batch, sink, top_k, recent,
+                           selected, s);
+  };
   for (int i = 0; i < Bs; ++i)
     for (int t = 0; t < n_new[i]; ++t) {
-      const int tok = i * C + t;
+      const int r = cache_rows[i], slot = slots_of(c, r) + t, tok = i * C + t;
       if (!batch.empty() &&
           ((int)batch.size() == kMaxRowsPerLaunch || tok - batch[0].tok > 0xffff)) {
-        rc = attend_selected(c, layer, (const __nv_bfloat16 *)q, (__nv_bfloat16 *)out, batch, sink,
-                             top_k, recent, selected, s);
-        if (rc != KV_OK) return rc;
+        if ((rc = flush()) != KV_OK) return rc;
         batch.clear();
       }
-      batch.push_back({cache_rows[i], slots_of(c, cache_rows[i]) + t,
-                       c->lens[cache_rows[i]] + t, tok});
+      SelectQuery sq = {r, slot, c->lens[r] + t, tok, 0, 0};
+      if (fused) {  // blocks complete with this token; known from now on up to the cached ones
+        sq.pend0 = valid[r];
+        sq.n_pend = std::max(0, (slot + 1) / kSparseBlock - valid[r]);
+        valid[r] = std::max(valid[r], slot / kSparseBlock);
+      }
+      batch.push_back(sq);
     }
-  return attend_selected(c, layer, (const __nv_bfloat16 *)q, (__nv_bfloat16 *)out, batch, sink,
-                         top_k, recent, selected, s);
+  return flush();
 }
 
 }  // extern "C"

@@ -333,13 +333,20 @@ struct SelectQuery {
   int32_t cache_row;
   int32_t slot;  // storage slot of the token's own key
   int32_t pos;   // its position
-  int32_t tok;   // its index in q and `selected`
+  int32_t tok;   // its index in q, k, v and `selected`
+  int32_t pend0, n_pend;  // with k: the row's complete blocks that have no bounds yet
 };
 struct SelectParams {
   const __nv_bfloat16 *q;  // [tok][Hq][D], pre-RoPE
   const float2 *rope;
-  const int8_t *bound;     // as BoundsParams
-  const float *scale;
+  int8_t *bound;           // as BoundsParams
+  float *scale;
+  // Calls of single-token rows: the launch appends the tokens itself (k, v [tok][Hk][D])
+  // and computes the pending bounds.  k == nullptr: launches before it have done both.
+  const __nv_bfloat16 *k, *v;
+  __nv_bfloat16 *cache_k, *cache_v;  // layer storage
+  int seg_rows;
+  PageTable pt;
   int32_t *list;           // [query of the launch][Hk][list_stride]
   int32_t *selected;       // [tok][Hk][sink + top_k + recent] or nullptr
   int Hq, Hk, rep, D, nb_cap, list_stride;

@@ -44,19 +44,14 @@ __device__ __forceinline__ int level(float x) {  // to -127 .. 127; NaN gives -1
   return __float2int_rn(fminf(fmaxf(x, -127.f), 127.f));
 }
 
-// One warp per (block, kv head).  A lane owns a 16-byte chunk of the head dimension and
-// every (32 / chunks)-th key; loads of eight keys are in flight at a time.
+// Bounds of block `blk` of (row, kv head), by one warp.  A lane owns a 16-byte chunk of the
+// head dimension and every (32 / chunks)-th key; loads of eight keys are in flight at a time.
 template <int D>
-__global__ void __launch_bounds__(kBoundsWarps * 32)
-    bounds_kernel(const __grid_constant__ BoundsParams p) {
-  ptx::grid_dep_wait();  // the keys come from the launches before
-  ptx::grid_dep_launch();
+__device__ __forceinline__ void bounds_of_block(const __nv_bfloat16 *K, const PageTable &pt,
+                                                int seg_rows, int cache_row, int Hk, int g, int blk,
+                                                int nb_cap, int8_t *bound, float *scale,
+                                                int lane) {
   constexpr int kChunks = D / 8, kKeysPer = 32 / kChunks;
-  const int item = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (item >= p.n_items) return;
-  const int g = blockIdx.y;
-  const BoundsRow &row = p.rows[find_bounds_row(p, item)];
-  const int blk = row.blk0 + item - row.item0;
   const int chunk = lane % kChunks, key0 = lane / kChunks;
   float lo[8], hi[8];
 #pragma unroll
@@ -70,8 +65,8 @@ __global__ void __launch_bounds__(kBoundsWarps * 32)
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int slot = blk * kSparseBlock + k0 + i * kKeysPer + key0;
-      x[i] = *reinterpret_cast<const uint4 *>(
-          p.K + kv_row(p.pt, row.cache_row, p.Hk, g, p.seg_rows, slot) * D + 8 * chunk);
+      x[i] = *reinterpret_cast<const uint4 *>(K + kv_row(pt, cache_row, Hk, g, seg_rows, slot) * D +
+                                              8 * chunk);
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -98,7 +93,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32)
   for (int off = 1; off < kChunks; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   const bool some = m >= kTiny;
   const float inv = some ? __fdiv_rn(127.f, m) : 0.f;
-  const int64_t at = ((int64_t)row.cache_row * p.Hk + g) * p.nb_cap + blk;
+  const int64_t at = ((int64_t)cache_row * Hk + g) * nb_cap + blk;
   if (lane < kChunks) {
     uint32_t h[2] = {0, 0}, l[2] = {0, 0};
 #pragma unroll
@@ -106,15 +101,31 @@ __global__ void __launch_bounds__(kBoundsWarps * 32)
       h[j / 4] |= (uint32_t)(level(ceilf(__fmul_rn(hi[j], inv))) & 255) << (8 * (j % 4));
       l[j / 4] |= (uint32_t)(level(floorf(__fmul_rn(lo[j], inv))) & 255) << (8 * (j % 4));
     }
-    uint2 *dst = reinterpret_cast<uint2 *>(p.bound + at * 2 * D);
+    uint2 *dst = reinterpret_cast<uint2 *>(bound + at * 2 * D);
     dst[chunk] = make_uint2(h[0], h[1]);
     dst[D / 8 + chunk] = make_uint2(l[0], l[1]);
-    if (lane == 0) p.scale[at] = some ? __fmul_rn(m, kStep) : 0.f;
+    if (lane == 0) scale[at] = some ? __fmul_rn(m, kStep) : 0.f;
   }
 }
 
+// One warp per (block, kv head).
+template <int D>
+__global__ void __launch_bounds__(kBoundsWarps * 32)
+    bounds_kernel(const __grid_constant__ BoundsParams p) {
+  ptx::grid_dep_wait();  // the keys come from the launches before
+  ptx::grid_dep_launch();
+  const int item = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5);
+  if (item >= p.n_items) return;
+  const BoundsRow &row = p.rows[find_bounds_row(p, item)];
+  bounds_of_block<D>(p.K, p.pt, p.seg_rows, row.cache_row, p.Hk, blockIdx.y,
+                     row.blk0 + item - row.item0, p.nb_cap, p.bound, p.scale, threadIdx.x & 31);
+}
+
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 128, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+// Up to this many candidates a block's rank is counted directly (every candidate against
+// every other), above it found by radix selection.
+constexpr int kCountMax = kSelThreads;
 
 // Order-preserving whole number of a score: NaN lowest, -0 and +0 alike.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -126,8 +137,28 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 template <int D>  // q+ and q- levels and steps of up to kMaxRep heads
 constexpr int kSelHead = kMaxRep * 2 * D + kMaxRep * 4;
 
-// One CTA per (query, kv head).
-template <int D>
+template <int W>  // W consecutive 4-byte words
+struct Words {
+  int w[W];
+};
+template <int W>
+__device__ __forceinline__ Words<W> load_words(const void *p) {
+  Words<W> r;
+  if constexpr (W == 4) {
+    const int4 x = *reinterpret_cast<const int4 *>(p);
+    r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+  } else {
+    static_assert(W == 2, "D is 64 or 128");
+    const int2 x = *reinterpret_cast<const int2 *>(p);
+    r.w[0] = x.x, r.w[1] = x.y;
+  }
+  return r;
+}
+
+// One CTA per (query, kv head).  APPEND (calls of single-token rows): the CTA first rotates
+// and stores its row's new key and value, and computes the bounds of the row's pending
+// blocks, so that a step needs no launches of their own for them.
+template <int D, bool APPEND>
 __global__ void __launch_bounds__(kSelThreads)
     select_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kHalf = D / 2;
@@ -137,7 +168,7 @@ __global__ void __launch_bounds__(kSelThreads)
   uint32_t *keys = reinterpret_cast<uint32_t *>(sm + kSelHead<D>);  // [max_cand]
   __shared__ int hist[256];
   __shared__ int warp_n[kSelWarps][2];
-  __shared__ int pick[2];  // the digit that holds the threshold, keys above it
+  __shared__ int pick[3];  // the digit that holds the threshold, keys above it and in it
 
   const SelectQuery &qu = p.queries[blockIdx.x];
   const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -148,8 +179,76 @@ __global__ void __launch_bounds__(kSelThreads)
   int32_t *list = p.list + ((int64_t)blockIdx.x * p.Hk + g) * p.list_stride;
   int32_t *user = p.selected ? p.selected + ((int64_t)qu.tok * p.Hk + g) * per : nullptr;
 
-  ptx::grid_dep_wait();  // bounds, and the lists that the launch before read
-  ptx::grid_dep_launch();
+  // APPEND: q, k and v may come from the kernel before; else an append of this call lies
+  // between, and whatever ran before that append has completed.
+  if (APPEND) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+  }
+  const float2 *cs = p.rope + (int64_t)qu.pos * kHalf;
+  if (APPEND && warp == kSelWarps - 1) {  // the new key and value, 8 pairs per lane
+    const int64_t dst = kv_row(p.pt, qu.cache_row, p.Hk, g, p.seg_rows, qu.slot) * D;
+    const int64_t src = ((int64_t)qu.tok * p.Hk + g) * D;
+    if (lane < kHalf / 8) {
+      const uint4 k1 = *reinterpret_cast<const uint4 *>(p.k + src + 8 * lane);
+      const uint4 k2 = *reinterpret_cast<const uint4 *>(p.k + src + kHalf + 8 * lane);
+      const __nv_bfloat16 *x1 = reinterpret_cast<const __nv_bfloat16 *>(&k1);
+      const __nv_bfloat16 *x2 = reinterpret_cast<const __nv_bfloat16 *>(&k2);
+      uint4 o1, o2;
+      __nv_bfloat16 *y1 = reinterpret_cast<__nv_bfloat16 *>(&o1);
+      __nv_bfloat16 *y2 = reinterpret_cast<__nv_bfloat16 *>(&o2);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float a = __bfloat162float(x1[j]), b = __bfloat162float(x2[j]);
+        const float2 e = cs[8 * lane + j];
+        y1[j] = __float2bfloat16_rn(__fsub_rn(__fmul_rn(a, e.x), __fmul_rn(b, e.y)));
+        y2[j] = __float2bfloat16_rn(__fadd_rn(__fmul_rn(a, e.y), __fmul_rn(b, e.x)));
+      }
+      *reinterpret_cast<uint4 *>(p.cache_k + dst + 8 * lane) = o1;
+      *reinterpret_cast<uint4 *>(p.cache_k + dst + kHalf + 8 * lane) = o2;
+    } else if (lane < kHalf / 8 + D / 8) {
+      const int c = lane - kHalf / 8;
+      *reinterpret_cast<uint4 *>(p.cache_v + dst + 8 * c) =
+          *reinterpret_cast<const uint4 *>(p.v + src + 8 * c);
+    }
+  }
+  if (n_cand > 0) {
+    // The group's query heads, one warp each: rotate (float products without contraction,
+    // one rounding to bf16, as the attention does), find the largest magnitude, quantise.
+    for (int h = warp; h < p.rep; h += kSelWarps) {
+      const __nv_bfloat16 *q = p.q + ((int64_t)qu.tok * p.Hq + g * p.rep + h) * D;
+      float a[kHalf / 32], b[kHalf / 32], m = 0.f;
+#pragma unroll
+      for (int i = 0; i < kHalf / 32; ++i) {
+        const int d = lane + 32 * i;
+        const float x1 = __bfloat162float(q[d]), x2 = __bfloat162float(q[d + kHalf]);
+        const float2 r = cs[d];
+        a[i] = __bfloat162float(
+            __float2bfloat16_rn(__fsub_rn(__fmul_rn(x1, r.x), __fmul_rn(x2, r.y))));
+        b[i] = __bfloat162float(
+            __float2bfloat16_rn(__fadd_rn(__fmul_rn(x1, r.y), __fmul_rn(x2, r.x))));
+        m = fmaxf(m, fmaxf(fabsf(a[i]), fabsf(b[i])));
+      }
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      const bool some = m >= kTiny;
+      const float inv = some ? __fdiv_rn(127.f, m) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kHalf / 32; ++i) {
+        const int d = lane + 32 * i;
+        const int la = level(rintf(__fmul_rn(a[i], inv))), lb = level(rintf(__fmul_rn(b[i], inv)));
+        q8[h * 2 * D + d] = (int8_t)max(la, 0);
+        q8[h * 2 * D + D + d] = (int8_t)min(la, 0);
+        q8[h * 2 * D + d + kHalf] = (int8_t)max(lb, 0);
+        q8[h * 2 * D + D + d + kHalf] = (int8_t)min(lb, 0);
+      }
+      if (lane == 0) qs[h] = some ? __fmul_rn(m, kStep) : 0.f;
+    }
+  }
+  if (!APPEND) {
+    ptx::grid_dep_wait();  // bounds, and the lists that the launch before read
+    ptx::grid_dep_launch();
+  }
   const auto put = [&](int i, int blk) {
     list[i] = blk;
     if (user) user[i] = blk;
@@ -158,90 +257,94 @@ __global__ void __launch_bounds__(kSelThreads)
     for (int i = n_sel + tid; i < per; i += kSelThreads) user[i] = -1;
   if (n_cand == 0) {  // everything there is
     for (int i = tid; i < n_sel; i += kSelThreads) put(i, i);
-    return;
+  } else {
+    for (int i = tid; i < p.sink; i += kSelThreads) put(i, i);
+    for (int i = tid; i < p.recent; i += kSelThreads)
+      put(p.sink + p.top_k + i, nb - p.recent + i);
   }
-  for (int i = tid; i < p.sink; i += kSelThreads) put(i, i);
-  for (int i = tid; i < p.recent; i += kSelThreads)
-    put(p.sink + p.top_k + i, nb - p.recent + i);
-
-  // The group's query heads, one warp each: rotate (float products without contraction,
-  // one rounding to bf16, as the attention does), find the largest magnitude, quantise.
-  const float2 *cs = p.rope + (int64_t)qu.pos * kHalf;
-  for (int h = warp; h < p.rep; h += kSelWarps) {
-    const __nv_bfloat16 *q = p.q + ((int64_t)qu.tok * p.Hq + g * p.rep + h) * D;
-    float a[kHalf / 32], b[kHalf / 32], m = 0.f;
-#pragma unroll
-    for (int i = 0; i < kHalf / 32; ++i) {
-      const int d = lane + 32 * i;
-      const float x1 = __bfloat162float(q[d]), x2 = __bfloat162float(q[d + kHalf]);
-      const float2 r = cs[d];
-      a[i] = __bfloat162float(
-          __float2bfloat16_rn(__fsub_rn(__fmul_rn(x1, r.x), __fmul_rn(x2, r.y))));
-      b[i] = __bfloat162float(
-          __float2bfloat16_rn(__fadd_rn(__fmul_rn(x1, r.y), __fmul_rn(x2, r.x))));
-      m = fmaxf(m, fmaxf(fabsf(a[i]), fabsf(b[i])));
-    }
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const bool some = m >= kTiny;
-    const float inv = some ? __fdiv_rn(127.f, m) : 0.f;
-#pragma unroll
-    for (int i = 0; i < kHalf / 32; ++i) {
-      const int d = lane + 32 * i;
-      const int la = level(rintf(__fmul_rn(a[i], inv))), lb = level(rintf(__fmul_rn(b[i], inv)));
-      q8[h * 2 * D + d] = (int8_t)max(la, 0);
-      q8[h * 2 * D + D + d] = (int8_t)min(la, 0);
-      q8[h * 2 * D + d + kHalf] = (int8_t)max(lb, 0);
-      q8[h * 2 * D + D + d + kHalf] = (int8_t)min(lb, 0);
-    }
-    if (lane == 0) qs[h] = some ? __fmul_rn(m, kStep) : 0.f;
+  __syncthreads();  // q8 and, APPEND, the stored key
+  if (APPEND && qu.n_pend > 0) {
+    for (int i = warp; i < qu.n_pend; i += kSelWarps)
+      bounds_of_block<D>(p.cache_k, p.pt, p.seg_rows, qu.cache_row, p.Hk, g, qu.pend0 + i,
+                         p.nb_cap, p.bound, p.scale, lane);
+    __syncthreads();
   }
-  __syncthreads();
+  if (n_cand == 0 || p.top_k == 0) return;
 
-  // Scores: eight lanes per block, each D / 8 of the head dimension.
+  // Scores: eight lanes per four blocks, each D / 8 of the head dimension; the four sums
+  // are spread over the lanes while they are added up, so that lanes 2 i and 2 i + 1 of the
+  // eight end with block i's.
   {
     constexpr int kWords = D / 32;  // 4-byte words per lane
     const int sub = tid & 7;
-    const int8_t *bound = p.bound + ((int64_t)qu.cache_row * p.Hk + g) * p.nb_cap * 2 * D;
+    const int8_t *bound = p.bound + ((int64_t)qu.cache_row * p.Hk + g) * p.nb_cap * 2 * D +
+                          4 * kWords * sub;
     const float *scale = p.scale + ((int64_t)qu.cache_row * p.Hk + g) * p.nb_cap;
     // every lane of a warp takes the same number of passes (the shuffles below)
-    for (int c0 = 0; c0 < n_cand; c0 += kSelThreads / 8) {
-      const int c = c0 + tid / 8;
-      const int blk = p.sink + min(c, n_cand - 1);
-      const int *hi = reinterpret_cast<const int *>(bound + (int64_t)blk * 2 * D) + sub * kWords;
-      const int *lo = hi + D / 4;
-      int h4[kWords], l4[kWords];
+    for (int c0 = 0; c0 < n_cand; c0 += kSelThreads / 2) {
+      const int cg = c0 + 4 * (tid / 8);
+      Words<kWords> hi[4], lo[4];
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        h4[w] = hi[w];
-        l4[w] = lo[w];
+      for (int i = 0; i < 4; ++i) {
+        const int8_t *b = bound + (int64_t)(p.sink + min(cg + i, n_cand - 1)) * 2 * D;
+        hi[i] = load_words<kWords>(b);
+        lo[i] = load_words<kWords>(b + D);
       }
-      const float st = scale[blk];
+      const int c = cg + (sub >> 1);
+      const float st = scale[p.sink + min(c, n_cand - 1)];
       uint32_t best = 0;
       for (int h = 0; h < p.rep; ++h) {
-        const int *qp = reinterpret_cast<const int *>(q8 + h * 2 * D) + sub * kWords;
-        int dot = 0;
+        const int8_t *qp = q8 + h * 2 * D + 4 * kWords * sub;
+        const Words<kWords> qa = load_words<kWords>(qp), qb = load_words<kWords>(qp + D);
+        int dot[4];
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-          dot = __dp4a(h4[w], qp[w], dot);
-          dot = __dp4a(l4[w], qp[D / 4 + w], dot);
+        for (int i = 0; i < 4; ++i) {
+          dot[i] = 0;
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            dot[i] = __dp4a(hi[i].w[w], qa.w[w], dot[i]);
+            dot[i] = __dp4a(lo[i].w[w], qb.w[w], dot[i]);
+          }
         }
-#pragma unroll
-        for (int off = 1; off < 8; off <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        best = max(best, order_key(__fmul_rn((float)dot, __fmul_rn(qs[h], st))));
+        const bool up = sub & 4, odd = sub & 2;
+        const int k0 = up ? dot[2] : dot[0], k1 = up ? dot[3] : dot[1];
+        const int s0 = up ? dot[0] : dot[2], s1 = up ? dot[1] : dot[3];
+        const int r0 = k0 + __shfl_xor_sync(0xffffffffu, s0, 4);
+        const int r1 = k1 + __shfl_xor_sync(0xffffffffu, s1, 4);
+        int d = (odd ? r1 : r0) + __shfl_xor_sync(0xffffffffu, odd ? r0 : r1, 2);
+        d += __shfl_xor_sync(0xffffffffu, d, 1);
+        best = max(best, order_key(__fmul_rn((float)d, __fmul_rn(qs[h], st))));
       }
-      if (sub == 0 && c < n_cand) keys[c] = best;
+      if ((sub & 1) == 0 && c < n_cand) keys[c] = best;
     }
   }
-  if (p.top_k == 0) return;
   __syncthreads();
 
+  uint32_t prefix = 0;  // keys above it are taken, and the first `ties` at it
+  int ties = 0;
+  if (n_cand <= kCountMax) {
+    // Each thread ranks one candidate; the taken ones are written in order.
+    const uint32_t mine = tid < n_cand ? keys[tid] : 0;
+    int rank = 0;
+    for (int j = 0; j < n_cand; ++j) {
+      const uint32_t x = keys[j];
+      rank += x > mine || (x == mine && j < tid);
+    }
+    const bool take = tid < n_cand && rank < p.top_k;
+    const uint32_t bt = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) warp_n[warp][0] = __popc(bt);
+    __syncthreads();
+    int at = __popc(bt & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) at += warp_n[w][0];
+    if (take) put(p.sink + at, p.sink + tid);
+    return;
+  }
   // The top_k-th largest key, one 8-bit digit at a time: `above` keys are larger than the
-  // prefix found so far, and the next digit is the one whose bin holds rank top_k.
-  uint32_t prefix = 0;
+  // prefix found so far, and the next digit is the one whose bin holds rank top_k.  When the
+  // whole bin is taken the rest of the digits do not matter.
   int above = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    hist[tid] = 0;
     __syncthreads();
     const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
     for (int c = tid; c < n_cand; c += kSelThreads)
@@ -264,6 +367,7 @@ __global__ void __launch_bounds__(kSelThreads)
           if (run + n >= p.top_k) {
             pick[0] = 255 - 8 * lane - i;
             pick[1] = run;
+            pick[2] = n;
             break;
           }
           run += n;
@@ -273,14 +377,19 @@ __global__ void __launch_bounds__(kSelThreads)
     __syncthreads();
     prefix |= (uint32_t)pick[0] << shift;
     above = pick[1];
+    ties = p.top_k - above;
+    if (pick[2] == ties && prefix > 0) {  // every key from the prefix on
+      prefix -= 1;
+      ties = 0;
+      break;
+    }
   }
-  // Blocks above the threshold, and the first top_k - above at it, in ascending order.
-  const int ties = p.top_k - above;
   int base_gt = 0, base_eq = 0;
   for (int c0 = 0; c0 < n_cand; c0 += kSelThreads) {
     const int c = c0 + tid;
     const uint32_t key = c < n_cand ? keys[c] : 0;
-    const bool gt = c < n_cand && key > prefix, eq = c < n_cand && key == prefix;
+    const bool gt = c < n_cand && key > prefix;
+    const bool eq = ties > 0 && c < n_cand && key == prefix;
     const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
     if (lane == 0) {
       warp_n[warp][0] = __popc(bg);
@@ -307,7 +416,20 @@ __global__ void __launch_bounds__(kSelThreads)
 template <int D>
 cudaError_t launch_select_t(const SelectParams &p, cudaStream_t s, bool pdl) {
   const int smem = kSelHead<D> + 4 * p.max_cand;
-  return launch_k(select_kernel<D>, dim3(p.n_queries, p.Hk), dim3(kSelThreads), smem, s, p, pdl);
+  const dim3 grid(p.n_queries, p.Hk), block(kSelThreads);
+  return p.k ? launch_k(select_kernel<D, true>, grid, block, smem, s, p, pdl)
+             : launch_k(select_kernel<D, false>, grid, block, smem, s, p, pdl);
+}
+
+// Keys of the longest row (max_len = 2^20: 16384 blocks) take 64 KB of shared memory.
+template <int D>
+cudaError_t configure_select_t() {
+  constexpr int smem = kSelHead<D> + 4 * ((1 << 20) / kSparseBlock);
+  const cudaError_t e = cudaFuncSetAttribute(
+      select_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(select_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              smem);
 }
 
 }  // namespace
@@ -324,15 +446,9 @@ cudaError_t launch_select(const SelectParams &p, cudaStream_t s, bool pdl) {
   return p.D == 128 ? launch_select_t<128>(p, s, pdl) : launch_select_t<64>(p, s, pdl);
 }
 
-// Keys of the longest row (max_len = 2^20: 16384 blocks) take 64 KB of shared memory.
 cudaError_t configure_select() {
-  constexpr int cand = (1 << 20) / kSparseBlock;
-  const cudaError_t e =
-      cudaFuncSetAttribute(select_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSelHead<128> + 4 * cand);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(select_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kSelHead<64> + 4 * cand);
+  const cudaError_t e = configure_select_t<128>();
+  return e == cudaSuccess ? configure_select_t<64>() : e;
 }
 
 }  // namespace kvinc
