@@ -386,6 +386,14 @@ int kvinc::plan_decode_splits(int num_sms, int Hk, int n, const int *nk2, Decode
   const int64_t target = (int64_t)num_sms * 2 * 4;
   int64_t per = (total_tiles * Hk + target - 1) / target;
   if (per < kMinDecodeSplitTiles) per = kMinDecodeSplitTiles;
+  // Listed blocks: a query's few tiles are split only while the launch leaves SMs idle.  A
+  // split costs a prologue, a partial and a share of a merge, as much as about ten tiles: 64
+  // queries x 8 heads x 19 blocks took 62 us with one split each, 71 with two and 74 with
+  // three; 16 x 8 x 37 took 44 us with one (128 CTAs), 54 with two and 63 with five.
+  if (p.list) {
+    const int64_t idle = std::max<int64_t>(1, num_sms / std::max<int64_t>(1, (int64_t)n * Hk));
+    per = std::max<int64_t>(kMinDecodeSplitTiles, (most_tiles + idle - 1) / idle);
+  }
   // splits of one segment: at most `cap`, each a whole number of tiles
   const auto splits = [&](int keys, int cap, int &st) {
     const int tiles = tiles_of(keys);
@@ -2338,7 +2346,7 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
   static const int no_ring[kMaxRowsPerLaunch] = {};
   // the partials are the cache's own: kMaxSplits slots for each of up to min(B, 512) rows
   plan_decode_splits(c->num_sms, Hk, n, no_ring, dp, std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
-  if (!c->pdl) dp.deep_pipeline = 0;
+  dp.deep_pipeline = 0;
   e = timed(c, KV_KERNEL_DECODE, kv_bytes + 4.0 * n * Hq * D, flops, s,
             [&] { return launch_decode(dp, D, dp.rep <= 8 ? 1 : 2, s, c->pdl); });
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
