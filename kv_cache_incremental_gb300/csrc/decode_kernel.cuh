@@ -287,20 +287,38 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
 
   if (LIST && warp == kConsumerWarps) {
     // ------------------------------------------------------------ producer (listed blocks)
-    // The lanes fetch 32 list entries (and, paged, their table entries) at a time, so that
-    // the tiles' addresses cost one memory round trip per 32 tiles; lane 0 issues the loads.
-    ptx::grid_dep_wait();  // the list comes from the launch before this one
-    const int32_t *list = p.list + ((int64_t)row_idx * p.Hk + g) * p.list_stride + k0 / kTileKeys;
+    // Tile order: the sink blocks, the recent blocks but the last, the chosen ones, the last
+    // block (all blocks in order when everything is listed).  Only the chosen ones have to
+    // be read from the list, and only the last block may be written by the launch before, so
+    // the others start to stream while the selection still runs.  The lanes fetch 32
+    // tiles' list entries (and, paged, table entries) at a time, one memory round trip per
+    // 32 tiles; lane 0 issues the loads.
+    const int last_blk = row.split_tiles2, tile_last = (row.nk - 1) / kTileKeys;
+    const bool all = tile_last == last_blk;
+    const int known = all ? tile_last : p.list_sink + p.list_recent - 1;
+    const int t0 = k0 / kTileKeys;
+    const int32_t *list = p.list + ((int64_t)row_idx * p.Hk + g) * p.list_stride - known;
     const int64_t head0 = ((int64_t)row.cache_row * p.Hk + g) * seg_rows;
+    bool waited = false;
+    const auto row_of = [&](int t) {
+      int blk = last_blk;
+      if (all || t < p.list_sink) blk = t;
+      else if (t < known) blk = last_blk - (known - t);
+      else if (t < tile_last) blk = list[t];
+      if (pt.max_blocks == 0)
+        return make_int4(static_cast<int>(head0 + (int64_t)blk * kTileKeys), 0, 0, 0);
+      return kv_rows4(pt, row.cache_row, g, blk * kTileKeys);
+    };
     int4 y4 = make_int4(0, 0, 0, 0);
+    if (t0 + lane < known && lane < n_tiles) y4 = row_of(t0 + lane);
     for (int it = 0; it < n_tiles; ++it) {
-      if (it % 32 == 0 && it + lane < n_tiles) {
-        const int blk = list[it + lane];
-        if (pt.max_blocks == 0)
-          y4.x = static_cast<int>(head0 + (int64_t)blk * kTileKeys);
-        else
-          y4 = kv_rows4(pt, row.cache_row, g, blk * kTileKeys);
+      if (!waited && (t0 + it >= known || (it % 32 == 0 && it > 0))) {
+        ptx::grid_dep_wait();  // the list, and the new key in the last block
+        waited = true;
+        const int t = t0 + it / 32 * 32 + lane;
+        if (t >= known && t < t0 + n_tiles) y4 = row_of(t);
       }
+      if (it % 32 == 0 && it > 0 && it + lane < n_tiles) y4 = row_of(t0 + it + lane);
       const int src = it % 32;
       int4 y;
       y.x = __shfl_sync(0xffffffffu, y4.x, src);
@@ -402,9 +420,12 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
   }
 
   // Inputs, partials, tickets and the cache are read or written only after the previous
-  // grid on the stream has completed; the next launch may then start.
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
+  // grid on the stream has completed; the next launch may then start.  A list launch follows
+  // the selection, which writes none of the queries: it waits after rotating them.
+  if (!LIST) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+  }
 
   // -------------------------------------------------------------- consumers
   {
@@ -485,6 +506,10 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
       }
       consumer_sync();  // the mini-tiles are complete before warp 0 reads them
     }
+  }
+  if (LIST) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
   }
   const int gq = lane >> 2;  // fragment row group
   const int qq = lane & 3;   // fragment column pair

@@ -2343,9 +2343,12 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
   dp.list = sp.list;
   dp.list_stride = sp.max_select;
   dp.scores = nullptr;
+  dp.list_sink = sink;
+  dp.list_recent = recent;
   static const int no_ring[kMaxRowsPerLaunch] = {};
   // the partials are the cache's own: kMaxSplits slots for each of up to min(B, 512) rows
   plan_decode_splits(c->num_sms, Hk, n, no_ring, dp, std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
+  for (int i = 0; i < n; ++i) dp.rows[i].split_tiles2 = qs[i].slot / kSparseBlock;
   dp.deep_pipeline = 0;
   e = timed(c, KV_KERNEL_DECODE, kv_bytes + 4.0 * n * Hq * D, flops, s,
             [&] { return launch_decode(dp, D, dp.rep <= 8 ? 1 : 2, s, c->pdl); });

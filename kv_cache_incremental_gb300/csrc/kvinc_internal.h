@@ -166,12 +166,14 @@ struct DecodeParams {  // 64-byte aligned through its CUtensorMap members
   // Host only: the launch fits one wave (n_items x Hk <= the SM count), so it runs the
   // variant with twice the K/V stages and one CTA per SM.
   int deep_pipeline;
-  // Sparse attention (the list variant of the kernel): tile t of row r's keys for kv head g
-  // is block list[(r * Hk + g) * list_stride + t] of the row's storage slots, and nk, splits
-  // and tiles count in that list.  The last listed block is the only one that may be partly
-  // filled.  nullptr: tile t is slots [64 t, 64 t + 64).
+  // Sparse attention (the list variant of the kernel): nk, splits and tiles of a row count
+  // in the blocks its query reads: the list_sink first ones, the list_recent last ones and,
+  // for kv head g, the chosen ones list[(r * Hk + g) * list_stride ...] of row r of the
+  // launch; DecodeRow::split_tiles2 holds the index of the last block, the only one that may
+  // be partly filled.  A row whose nk covers all of its blocks reads them all and no list.
+  // nullptr: tile t is slots [64 t, 64 t + 64).
   const int32_t *list;
-  int list_stride;
+  int list_stride, list_sink, list_recent;
   // Accumulated weights (the scores variant): head hq's score of slot j, in log2 units, goes
   // to scores[(r * Hq + hq) * score_stride + j] for row r of the launch, and the softmax
   // maximum and the reciprocal of its sum to row_ml[r * Hq + hq].  nullptr: neither.
@@ -328,7 +330,7 @@ struct BoundsParams {
   BoundsRow rows[kMaxRowsPerLaunch];
 };
 
-// One query token: its blocks, per kv head, in ascending order.
+// One query token whose blocks are chosen per kv head.
 struct SelectQuery {
   int32_t cache_row;
   int32_t slot;  // storage slot of the token's own key
@@ -347,7 +349,7 @@ struct SelectParams {
   __nv_bfloat16 *cache_k, *cache_v;  // layer storage
   int seg_rows;
   PageTable pt;
-  int32_t *list;           // [query of the launch][Hk][list_stride]
+  int32_t *list;           // [query of the launch][Hk][list_stride]: the chosen blocks
   int32_t *selected;       // [tok][Hk][sink + top_k + recent] or nullptr
   int Hq, Hk, rep, D, nb_cap, list_stride;
   int sink, top_k, recent;

@@ -249,18 +249,18 @@ __global__ void __launch_bounds__(kSelThreads)
     ptx::grid_dep_wait();  // bounds, and the lists that the launch before read
     ptx::grid_dep_launch();
   }
-  const auto put = [&](int i, int blk) {
+  const auto put = [&](int i, int blk) {  // the i-th chosen block, ascending
     list[i] = blk;
-    if (user) user[i] = blk;
+    if (user) user[p.sink + i] = blk;
   };
-  if (user)
-    for (int i = n_sel + tid; i < per; i += kSelThreads) user[i] = -1;
-  if (n_cand == 0) {  // everything there is
-    for (int i = tid; i < n_sel; i += kSelThreads) put(i, i);
-  } else {
-    for (int i = tid; i < p.sink; i += kSelThreads) put(i, i);
-    for (int i = tid; i < p.recent; i += kSelThreads)
-      put(p.sink + p.top_k + i, nb - p.recent + i);
+  if (user) {  // the blocks read in any case: everything there is, or the first and last ones
+    for (int i = tid; i < per; i += kSelThreads)
+      if (n_cand == 0)
+        user[i] = i < n_sel ? i : -1;
+      else if (i < p.sink)
+        user[i] = i;
+      else if (i >= p.sink + p.top_k)
+        user[i] = nb - per + i;
   }
   __syncthreads();  // q8 and, APPEND, the stored key
   if (APPEND && qu.n_pend > 0) {
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kSelThreads)
     __syncthreads();
     int at = __popc(bt & ((1u << lane) - 1));
     for (int w = 0; w < warp; ++w) at += warp_n[w][0];
-    if (take) put(p.sink + at, p.sink + tid);
+    if (take) put(at, p.sink + tid);
     return;
   }
   // The top_k-th largest key, one 8-bit digit at a time: `above` keys are larger than the
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kSelThreads)
     const uint32_t below = (1u << lane) - 1;
     ng += __popc(bg & below);
     ne += __popc(be & below);
-    if (gt || (eq && ne < ties)) put(p.sink + ng + min(ne, ties), p.sink + c);
+    if (gt || (eq && ne < ties)) put(ng + min(ne, ties), p.sink + c);
     __syncthreads();
   }
 }
