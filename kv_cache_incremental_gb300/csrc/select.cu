@@ -122,10 +122,9 @@ __global__ void __launch_bounds__(kBoundsWarps * 32)
 }
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 // Up to this many candidates a block's rank is counted directly (every candidate against
 // every other), above it found by radix selection.
-constexpr int kCountMax = kSelThreads;
+constexpr int kCountMax = 256;
 
 // Order-preserving whole number of a score: NaN lowest, -0 and +0 alike.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -158,9 +157,11 @@ __device__ __forceinline__ Words<W> load_words(const void *p) {
 // One CTA per (query, kv head).  APPEND (calls of single-token rows): the CTA first rotates
 // and stores its row's new key and value, and computes the bounds of the row's pending
 // blocks, so that a step needs no launches of their own for them.
-template <int D, bool APPEND>
-__global__ void __launch_bounds__(kSelThreads)
-    select_kernel(const __grid_constant__ SelectParams p) {
+// T threads.
+template <int D, bool APPEND, int T>
+__global__ void __launch_bounds__(T) select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kSelThreads = T, kSelWarps = T / 32;
+  static_assert(T >= kCountMax && T >= 256, "a thread per counted candidate and per bin");
   constexpr int kHalf = D / 2;
   extern __shared__ __align__(16) uint8_t sm[];
   int8_t *q8 = reinterpret_cast<int8_t *>(sm);                     // [rep][2][D]: q+, q-
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kSelThreads)
   // whole bin is taken the rest of the digits do not matter.
   int above = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
+    if (tid < 256) hist[tid] = 0;
     __syncthreads();
     const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
     for (int c = tid; c < n_cand; c += kSelThreads)
@@ -413,23 +414,36 @@ __global__ void __launch_bounds__(kSelThreads)
   }
 }
 
-template <int D>
+template <int D, bool APPEND, int T>
 cudaError_t launch_select_t(const SelectParams &p, cudaStream_t s, bool pdl) {
-  const int smem = kSelHead<D> + 4 * p.max_cand;
-  const dim3 grid(p.n_queries, p.Hk), block(kSelThreads);
-  return p.k ? launch_k(select_kernel<D, true>, grid, block, smem, s, p, pdl)
-             : launch_k(select_kernel<D, false>, grid, block, smem, s, p, pdl);
+  return launch_k(select_kernel<D, APPEND, T>, dim3(p.n_queries, p.Hk), dim3(T),
+                  kSelHead<D> + 4 * (size_t)p.max_cand, s, p, pdl);
 }
 
 // Keys of the longest row (max_len = 2^20: 16384 blocks) take 64 KB of shared memory.
-template <int D>
+template <int D, bool APPEND, int T>
 cudaError_t configure_select_t() {
   constexpr int smem = kSelHead<D> + 4 * ((1 << 20) / kSparseBlock);
-  const cudaError_t e = cudaFuncSetAttribute(
-      select_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(select_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smem);
+  return cudaFuncSetAttribute(select_kernel<D, APPEND, T>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+// Threads per CTA: TSMALL while the longest query's candidates fit two passes of scoring.
+constexpr int kSelSmall = 256, kSelLarge = 512;
+
+template <int D, bool APPEND>
+cudaError_t launch_select_d(const SelectParams &p, cudaStream_t s, bool pdl) {
+  return p.max_cand <= 256 ? launch_select_t<D, APPEND, kSelSmall>(p, s, pdl)
+                           : launch_select_t<D, APPEND, kSelLarge>(p, s, pdl);
+}
+
+template <int D>
+cudaError_t configure_select_d() {
+  cudaError_t e = configure_select_t<D, true, kSelSmall>();
+  if (e == cudaSuccess) e = configure_select_t<D, true, kSelLarge>();
+  if (e == cudaSuccess) e = configure_select_t<D, false, kSelSmall>();
+  if (e == cudaSuccess) e = configure_select_t<D, false, kSelLarge>();
+  return e;
 }
 
 }  // namespace
@@ -443,12 +457,14 @@ cudaError_t launch_bounds(const BoundsParams &p, cudaStream_t s, bool pdl) {
 
 cudaError_t launch_select(const SelectParams &p, cudaStream_t s, bool pdl) {
   if (p.n_queries <= 0) return cudaSuccess;
-  return p.D == 128 ? launch_select_t<128>(p, s, pdl) : launch_select_t<64>(p, s, pdl);
+  if (p.D == 128)
+    return p.k ? launch_select_d<128, true>(p, s, pdl) : launch_select_d<128, false>(p, s, pdl);
+  return p.k ? launch_select_d<64, true>(p, s, pdl) : launch_select_d<64, false>(p, s, pdl);
 }
 
 cudaError_t configure_select() {
-  const cudaError_t e = configure_select_t<128>();
-  return e == cudaSuccess ? configure_select_t<64>() : e;
+  const cudaError_t e = configure_select_d<128>();
+  return e == cudaSuccess ? configure_select_d<64>() : e;
 }
 
 }  // namespace kvinc
