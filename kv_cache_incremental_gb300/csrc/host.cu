@@ -2573,9 +2573,9 @@ int accumulate_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
           work += tiles(rows[r1].slots + rows[r1].t1);
           ++r1;
         }
-        // pass 1: about four CTAs per SM in all, splits of at least four tiles, longer until
+        // pass 1: about two CTAs per SM in all, splits of at least four tiles, longer until
         // the partials fit
-        int64_t per = std::max<int64_t>(4, (work * Hk + 4 * c->num_sms - 1) / (4 * c->num_sms));
+        int64_t per = std::max<int64_t>(4, (work * Hk + 2 * c->num_sms - 1) / (2 * c->num_sms));
         for (;; per *= 2) {
           int64_t part = 0;
           int item = 0, longest = 1;
@@ -2605,13 +2605,13 @@ int accumulate_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
         cudaError_t e = timed(c, KV_KERNEL_WEIGHTS, kb, fl, s,
                               [&] { return launch_weights(p, 1, s, c->pdl); });
         if (e != cudaSuccess) return KV_ERR_CUDA;
-        // pass 2: a CTA per key tile of every slot that the call defines
+        // pass 2: CTAs over every slot that the call defines
         int item = 0;
         double ab = 0;
         for (int j = 0; j < p.n_rows; ++j) {
           WeightsRow &r = p.rows[j];
           r.item0 = item;
-          item += tiles(r.slots + r.n);
+          item += (tiles(r.slots + r.n) + kWeightSumTiles - 1) / kWeightSumTiles;
           ab += 8.0 * (r.slots + r.n) * Hk;
         }
         p.n_items = item;

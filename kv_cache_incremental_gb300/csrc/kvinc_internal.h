@@ -375,7 +375,8 @@ struct WeightsRow {
   int32_t n_splits, split_tiles;  // of pass 1, in kWeightTile keys
   int32_t part;     // first (m, l) vector of the row
 };
-constexpr int kWeightTile = 128;  // keys per CTA and pass
+constexpr int kWeightTile = 128;   // keys per CTA and step
+constexpr int kWeightSumTiles = 4;  // tiles per CTA of pass 2
 struct WeightsParams {
   const __nv_bfloat16 *K;  // layer storage
   const __nv_bfloat16 *q;  // [Bs][C][Hq][D]

@@ -26,6 +26,7 @@ namespace kvinc {
 namespace {
 
 constexpr int kWarps = 8, kWThreads = kWarps * 32;
+constexpr int kSumTiles = kWeightSumTiles;
 static_assert(kWeightTile == kWarps * 16, "one 16-key fragment per warp");
 
 __device__ __forceinline__ int find_weights_row(const WeightsParams &p, int item) {
@@ -44,11 +45,16 @@ template <int D>
 constexpr int kQStride = 2 * D + 64;
 
 // Query vectors [v0, v0 + 8 QT) of the row, rotated and rounded to bf16 as the attention
-// rotates them, into shared memory; vectors past the last are zero.
+// rotates them, into shared memory, and the last slot that each sees; vectors past the last
+// are zero and see nothing.
 template <int D, int QT>
 __device__ __forceinline__ void load_queries(const WeightsParams &p, const WeightsRow &row, int g,
-                                             int v0, int n_vec, uint8_t *qs) {
+                                             int v0, int n_vec, uint8_t *qs, int *limit) {
   constexpr int kHalf = D / 2, kVec = kHalf / 8;
+  if (threadIdx.x < 8 * QT)
+    limit[threadIdx.x] = v0 + (int)threadIdx.x < n_vec
+                             ? row.slots + row.t0 + (v0 + (int)threadIdx.x) / p.rep
+                             : -1;
   for (int u = threadIdx.x; u < 8 * QT * kVec; u += kWThreads) {
     const int i = u / kVec, c = u % kVec, vec = v0 + i;
     uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
@@ -95,28 +101,108 @@ __device__ __forceinline__ void load_keys(const WeightsParams &p, const WeightsR
   }
 }
 
-// Scores of the warp's 16 keys with query vectors 8 nt .. 8 nt + 7 of the chunk in qs.
+// The loaded keys as MMA fragments, each in four consecutive registers as the instruction
+// takes them (formed once per 16 keys: left to the use of the loaded vectors themselves,
+// every MMA was preceded by the moves that gather its operand).
 template <int D>
-__device__ __forceinline__ void scores8(const uint4 (&a)[D / 32], const uint4 (&b)[D / 32],
-                                        const uint8_t *qs, int nt, int lane, float (&s)[4]) {
-  const int gq = lane >> 2, qq = lane & 3;
-  s[0] = s[1] = s[2] = s[3] = 0.f;
-  const uint8_t *qr = qs + (8 * nt + gq) * kQStride<D> + 16 * qq;
+__device__ __forceinline__ void fragments(const uint4 (&a)[D / 32], const uint4 (&b)[D / 32],
+                                          uint4 (&f)[D / 16]) {
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(qr + 64 * j);
-    ptx::mma_bf16(s, a[j].x, b[j].x, a[j].y, b[j].y, w.x, w.y);
-    ptx::mma_bf16(s, a[j].z, b[j].z, a[j].w, b[j].w, w.z, w.w);
+    f[2 * j] = make_uint4(a[j].x, b[j].x, a[j].y, b[j].y);
+    f[2 * j + 1] = make_uint4(a[j].z, b[j].z, a[j].w, b[j].w);
   }
 }
 
-// Pass 1: one CTA per (row, key split, kv head); (m, l) of every query vector over the
-// split's keys.
+// Scores of the warp's 16 keys with N eights of query vectors of the chunk in qs, from the
+// nt-th on; the eights' MMA chains are independent and interleaved.
+template <int D, int N>
+__device__ __forceinline__ void scores(const uint4 (&f)[D / 16], const uint8_t *qs, int nt,
+                                       int lane, float (&s)[N][4]) {
+  const int gq = lane >> 2, qq = lane & 3;
+  const uint8_t *qr = qs + (8 * nt + gq) * kQStride<D> + 16 * qq;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    uint4 w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      w[i] = *reinterpret_cast<const uint4 *>(qr + 8 * i * kQStride<D> + 64 * j);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint4 &x = f[2 * j];
+        if (j == 0)
+          ptx::mma_bf16_zero(s[i], x.x, x.y, x.z, x.w, w[i].x, w[i].y);
+        else
+          ptx::mma_bf16(s[i], x.x, x.y, x.z, x.w, w[i].x, w[i].y);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint4 &x = f[2 * j + 1];
+        ptx::mma_bf16(s[i], x.x, x.y, x.z, x.w, w[i].z, w[i].w);
+    }
+  }
+}
+
+// The exponent's reference of a query vector that has seen no key yet, and how far a score
+// may lie above the reference before the sum is rescaled: sums then stay below 2^(64 + 31).
+constexpr float kNoRef = -1e30f, kSlack = 64.f;
+
+// Pass 1: one CTA per (row, key split, kv head); a reference m and the sum l = sum_j 2^(x_j -
+// m) of every query vector over the split's keys.  m need not be the maximum: it moves only
+// when a score exceeds it by kSlack, so that a score costs one multiply-add, one ex2 and
+// one addition.
+//
+// One step: 16 keys as fragments f against the first n_nt eights of query vectors.  FULL: every key
+// is visible to every vector; else key gq is visible up to `limit` and below k1.
+template <int D, int QT, bool FULL>
+__device__ __forceinline__ void stats_step(const uint4 (&f)[D / 16], const uint8_t *qs,
+                                           const int *limit, int n_nt, int key, int k1,
+                                           float scale, int lane, float (&nm)[QT][2],
+                                           float (&l)[QT][2]) {
+  constexpr int N = QT > 1 ? 2 : 1;
+#pragma unroll
+  for (int nt0 = 0; nt0 < QT; nt0 += N) {
+    if (QT > 1 && nt0 >= n_nt) break;
+    float sc[N][4];
+    scores<D, N>(f, qs, nt0, lane, sc);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float(&s)[4] = sc[i];
+      const int nt = nt0 + i;
+      if (!FULL) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int lim = min(k1 - 1, limit[8 * nt + 2 * (lane & 3) + j]);
+          if (key > lim) s[j] = -INFINITY;
+          if (key + 8 > lim) s[2 + j] = -INFINITY;
+        }
+      }
+      float d0 = fmaf(s[0], scale, nm[nt][0]), d2 = fmaf(s[2], scale, nm[nt][0]);
+      float d1 = fmaf(s[1], scale, nm[nt][1]), d3 = fmaf(s[3], scale, nm[nt][1]);
+      if (__any_sync(0xffffffffu, fmaxf(fmaxf(d0, d2), fmaxf(d1, d3)) > kSlack)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float m = -nm[nt][j], mn = fmaxf(m, fmaxf(s[j] * scale, s[2 + j] * scale));
+          l[nt][j] *= ptx::ex2(m - mn);
+          nm[nt][j] = -mn;
+        }
+        d0 = fmaf(s[0], scale, nm[nt][0]);
+        d2 = fmaf(s[2], scale, nm[nt][0]);
+        d1 = fmaf(s[1], scale, nm[nt][1]);
+        d3 = fmaf(s[3], scale, nm[nt][1]);
+      }
+      l[nt][0] += ptx::ex2(d0) + ptx::ex2(d2);
+      l[nt][1] += ptx::ex2(d1) + ptx::ex2(d3);
+    }
+  }
+}
+
 template <int D, int QT>
-__global__ void __launch_bounds__(kWThreads)
+__global__ void __launch_bounds__(kWThreads, 2)
     weights_stats_kernel(const __grid_constant__ WeightsParams p) {
   __shared__ __align__(16) uint8_t qs[8 * QT * kQStride<D>];
   __shared__ float2 red[kWarps][8 * QT];
+  __shared__ int limit[8 * QT];
   const WeightsRow &row = p.rows[find_weights_row(p, blockIdx.x)];
   const int g = blockIdx.y, split = blockIdx.x - row.item0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, qq = lane & 3;
@@ -127,124 +213,158 @@ __global__ void __launch_bounds__(kWThreads)
   ptx::grid_dep_wait();  // keys come from the launches before; partials are read by them
   ptx::grid_dep_launch();
   for (int v0 = 0; v0 < n_vec; v0 += 8 * QT) {
+    const int n_nt = min(QT, (n_vec - v0 + 7) / 8);
+    uint4 a[D / 32], b[D / 32];
+    if (k0 + 16 * warp < k1) load_keys<D>(p, row, g, k0 + 16 * warp, keys - 1, lane, a, b);
     __syncthreads();
-    load_queries<D, QT>(p, row, g, v0, n_vec, qs);
+    load_queries<D, QT>(p, row, g, v0, n_vec, qs, limit);
     __syncthreads();
-    float m[QT][2], l[QT][2];
+    float nm[QT][2], l[QT][2];  // -m, l
 #pragma unroll
     for (int nt = 0; nt < QT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      nm[nt][0] = nm[nt][1] = -kNoRef;
       l[nt][0] = l[nt][1] = 0.f;
     }
     for (int kb = k0 + 16 * warp; kb < k1; kb += kWeightTile) {
-      uint4 a[D / 32], b[D / 32];
-      load_keys<D>(p, row, g, kb, keys - 1, lane, a, b);
-#pragma unroll
-      for (int nt = 0; nt < QT; ++nt) {
-        float s[4];
-        scores8<D>(a, b, qs, nt, lane, s);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {  // query vector of this column
-          const int limit = row.slots + row.t0 + (v0 + 8 * nt + 2 * qq + j) / p.rep;
-          const float x0 = kb + gq < k1 && kb + gq <= limit ? s[j] * p.scale_log2 : -INFINITY;
-          const float x1 =
-              kb + gq + 8 < k1 && kb + gq + 8 <= limit ? s[2 + j] * p.scale_log2 : -INFINITY;
-          const float mn = fmaxf(m[nt][j], fmaxf(x0, x1));
-          const float base = mn == -INFINITY ? 0.f : mn;
-          l[nt][j] = l[nt][j] * exp2f(m[nt][j] - base) + (exp2f(x0 - base) + exp2f(x1 - base));
-          m[nt][j] = mn;
-        }
-      }
+      uint4 f[D / 16];
+      fragments<D>(a, b, f);
+      if (kb + kWeightTile < k1)  // the next keys, while these are used
+        load_keys<D>(p, row, g, kb + kWeightTile, keys - 1, lane, a, b);
+      if (kb + 16 <= k1 && kb + 15 <= row.slots + row.t0)
+        stats_step<D, QT, true>(f, qs, limit, n_nt, kb + gq, k1, p.scale_log2, lane, nm, l);
+      else
+        stats_step<D, QT, false>(f, qs, limit, n_nt, kb + gq, k1, p.scale_log2, lane, nm, l);
     }
 #pragma unroll
-    for (int nt = 0; nt < QT; ++nt)
+    for (int nt = 0; nt < QT; ++nt) {
+      if (QT > 1 && nt >= n_nt) break;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float mm = m[nt][j], ll = l[nt][j];
+        const float m = -nm[nt][j];
+        float mm = m;
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          const float mo = __shfl_xor_sync(0xffffffffu, mm, off);
-          const float lo = __shfl_xor_sync(0xffffffffu, ll, off);
-          const float mn = fmaxf(mm, mo), base = mn == -INFINITY ? 0.f : mn;
-          ll = ll * exp2f(mm - base) + lo * exp2f(mo - base);
-          mm = mn;
-        }
+        for (int off = 4; off < 32; off <<= 1)
+          mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
+        float ll = l[nt][j] * ptx::ex2(m - mm);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
         if (gq == 0) red[warp][8 * nt + 2 * qq + j] = make_float2(mm, ll);
       }
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < 8 * QT; i += kWThreads) {
       if (v0 + i >= n_vec) continue;
-      float mm = -INFINITY, ll = 0.f;
+      float mm = kNoRef, ll = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, red[w][i].x);
-      const float base = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) ll += red[w][i].y * exp2f(red[w][i].x - base);
+      for (int w = 0; w < kWarps; ++w) ll += red[w][i].y * ptx::ex2(red[w][i].x - mm);
       p.part_ml[row.part + (int64_t)(split * p.Hk + g) * n_vec + v0 + i] = make_float2(mm, ll);
     }
   }
 }
 
-// Pass 2: one CTA per (row, 128-key tile, kv head).
+// Pass 2: one CTA per (row, kSumTiles tiles of 128 keys, kv head).  One step as in pass 1;
+// ml holds -m and the reciprocal of the sum.
+template <int D, int QT, bool FULL>
+__device__ __forceinline__ void sum_step(const uint4 (&f)[D / 16], const uint8_t *qs,
+                                         const int *limit, const float2 *ml,
+                                         int n_nt, int key, float scale, int lane, float &sum0,
+                                         float &sum1) {
+  constexpr int N = QT > 1 ? 2 : 1;
+#pragma unroll
+  for (int nt0 = 0; nt0 < QT; nt0 += N) {
+    if (QT > 1 && nt0 >= n_nt) break;
+    float sc[N][4];
+    scores<D, N>(f, qs, nt0, lane, sc);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float(&s)[4] = sc[i];
+      const int nt = nt0 + i;
+      const float4 e = *reinterpret_cast<const float4 *>(&ml[8 * nt + 2 * (lane & 3)]);
+      float w0 = ptx::ex2(fmaf(s[0], scale, e.x)), w1 = ptx::ex2(fmaf(s[1], scale, e.z));
+      float w2 = ptx::ex2(fmaf(s[2], scale, e.x)), w3 = ptx::ex2(fmaf(s[3], scale, e.z));
+      if (!FULL) {
+        const int l0 = limit[8 * nt + 2 * (lane & 3)], l1 = limit[8 * nt + 2 * (lane & 3) + 1];
+        if (key > l0) w0 = 0.f;
+        if (key > l1) w1 = 0.f;
+        if (key + 8 > l0) w2 = 0.f;
+        if (key + 8 > l1) w3 = 0.f;
+      }
+      sum0 = fmaf(w0, e.y, fmaf(w1, e.w, sum0));
+      sum1 = fmaf(w2, e.y, fmaf(w3, e.w, sum1));
+    }
+  }
+}
+
 template <int D, int QT>
-__global__ void __launch_bounds__(kWThreads)
+__global__ void __launch_bounds__(kWThreads, 2)
     weights_sum_kernel(const __grid_constant__ WeightsParams p) {
   __shared__ __align__(16) uint8_t qs[8 * QT * kQStride<D>];
-  __shared__ float2 ml[8 * QT];  // max, 1 / sum of the chunk's query vectors
+  __shared__ __align__(16) float2 ml[8 * QT];
+  __shared__ int limit[8 * QT];
   const WeightsRow &row = p.rows[find_weights_row(p, blockIdx.x)];
-  const int g = blockIdx.y, tile = blockIdx.x - row.item0;
+  const int g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, qq = lane & 3;
   const int n_vec = (row.t1 - row.t0) * p.rep;
   const int keys = row.slots + row.n;  // slots whose accumulator the call defines
-  const int kb = tile * kWeightTile + 16 * warp;
+  const int kb0 = (blockIdx.x - row.item0) * kSumTiles * kWeightTile + 16 * warp;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  uint4 a[D / 32], b[D / 32];
-  load_keys<D>(p, row, g, kb, keys - 1, lane, a, b);
-  float sum0 = 0.f, sum1 = 0.f;
+  float sum[kSumTiles][2];
+#pragma unroll
+  for (int i = 0; i < kSumTiles; ++i) sum[i][0] = sum[i][1] = 0.f;
   for (int v0 = 0; v0 < n_vec; v0 += 8 * QT) {
+    const int n_nt = min(QT, (n_vec - v0 + 7) / 8);
+    uint4 a[D / 32], b[D / 32];
+    load_keys<D>(p, row, g, kb0, keys - 1, lane, a, b);
     __syncthreads();
-    load_queries<D, QT>(p, row, g, v0, n_vec, qs);
+    load_queries<D, QT>(p, row, g, v0, n_vec, qs, limit);
     for (int i = threadIdx.x; i < 8 * QT; i += kWThreads) {
-      float mm = -INFINITY, ll = 0.f;
+      float mm = kNoRef, ll = 0.f;
       if (v0 + i < n_vec) {
         const float2 *part = p.part_ml + row.part + (int64_t)g * n_vec + v0 + i;
         const int64_t stride = (int64_t)p.Hk * n_vec;
         for (int s = 0; s < row.n_splits; ++s) mm = fmaxf(mm, part[s * stride].x);
         for (int s = 0; s < row.n_splits; ++s) {
           const float2 x = part[s * stride];
-          ll += x.y * exp2f(x.x - mm);
+          ll += x.y * ptx::ex2(x.x - mm);
         }
       }
-      ml[i] = make_float2(mm, 1.f / ll);
+      // a vector past the last: weights 2^(0 - inf) * 0
+      ml[i] = v0 + i < n_vec ? make_float2(-mm, 1.f / ll) : make_float2(-INFINITY, 0.f);
     }
     __syncthreads();
 #pragma unroll
-    for (int nt = 0; nt < QT; ++nt) {
-      if (v0 + 8 * nt >= n_vec) break;
-      float s[4];
-      scores8<D>(a, b, qs, nt, lane, s);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int vec = v0 + 8 * nt + 2 * qq + j;
-        const int limit = vec < n_vec ? row.slots + row.t0 + vec / p.rep : -1;
-        const float2 e = ml[8 * nt + 2 * qq + j];
-        if (kb + gq <= limit) sum0 += exp2f(s[j] * p.scale_log2 - e.x) * e.y;
-        if (kb + gq + 8 <= limit) sum1 += exp2f(s[2 + j] * p.scale_log2 - e.x) * e.y;
-      }
+    for (int i = 0; i < kSumTiles; ++i) {
+      const int kb = kb0 + i * kWeightTile;
+      if (kb >= keys) break;
+      uint4 f[D / 16];
+      fragments<D>(a, b, f);
+      if (i + 1 < kSumTiles && kb + kWeightTile < keys)
+        load_keys<D>(p, row, g, kb + kWeightTile, keys - 1, lane, a, b);
+      if (kb + 15 <= row.slots + row.t0)
+        sum_step<D, QT, true>(f, qs, limit, ml, n_nt, kb + gq, p.scale_log2, lane, sum[i][0],
+                              sum[i][1]);
+      else
+        sum_step<D, QT, false>(f, qs, limit, ml, n_nt, kb + gq, p.scale_log2, lane, sum[i][0],
+                               sum[i][1]);
     }
   }
 #pragma unroll
-  for (int off = 1; off < 4; off <<= 1) {
-    sum0 += __shfl_xor_sync(0xffffffffu, sum0, off);
-    sum1 += __shfl_xor_sync(0xffffffffu, sum1, off);
-  }
-  if (qq < 2) {  // lanes 0 and 1 of a quad write its two keys
-    const int slot = kb + gq + 8 * qq;
-    const int64_t at = ((int64_t)row.cache_row * p.Hk + g) * p.acc_stride + slot;
-    if (slot < keys) {
-      const float before = slot < row.slots || !row.first ? p.acc_in[at] : 0.f;
-      p.acc_out[at] = before + (qq == 0 ? sum0 : sum1);
+  for (int i = 0; i < kSumTiles; ++i) {
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      sum[i][0] += __shfl_xor_sync(0xffffffffu, sum[i][0], off);
+      sum[i][1] += __shfl_xor_sync(0xffffffffu, sum[i][1], off);
+    }
+    if (qq < 2) {  // lanes 0 and 1 of a quad write its two keys
+      const int slot = kb0 + i * kWeightTile + gq + 8 * qq;
+      const int64_t at = ((int64_t)row.cache_row * p.Hk + g) * p.acc_stride + slot;
+      if (slot < keys) {
+        const float before = slot < row.slots || !row.first ? p.acc_in[at] : 0.f;
+        p.acc_out[at] = before + (qq == 0 ? sum[i][0] : sum[i][1]);
+      }
     }
   }
 }
