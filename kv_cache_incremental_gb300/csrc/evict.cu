@@ -8,7 +8,7 @@
 // The choice is a radix selection: the (keep - recent)-th largest weight is found 11, 11
 // and 10 bits at a time from histograms of the order-preserving whole numbers of the
 // weights, then the slots above it (and the first of its ties) are written in order from
-// per-warp counts.  One CTA per (row, layer, kv head); the numbers stay in shared memory
+// per-warp counts.  One CTA per (row, layer, kv head); the weights stay in shared memory
 // while they fit.
 #include "kvinc_internal.h"
 #include "ptx.cuh"
@@ -27,112 +27,155 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// HELD: the row's weights stay in shared memory (every launch whose rows fit).
 template <bool HELD>
 __global__ void __launch_bounds__(kThreads)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t held[];
+  extern __shared__ float held[];
   __shared__ int hist[kBins];
   __shared__ int warp_n[kWarps][2];
-  __shared__ int pick[2];
+  __shared__ int pick[3];  // the digit that holds the threshold, keys above it and in it
   const EvictItem &it = p.items[blockIdx.x];
   const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float *acc = it.acc_in + (int64_t)g * p.acc_in_stride;
+  float *out = it.acc_out ? it.acc_out + (int64_t)g * p.acc_out_stride : nullptr;
   int32_t *kept = it.kept + (int64_t)g * p.keep;
-  const int m = min(it.slots, p.keep);
+  const bool cut = it.slots > p.keep;
+  const int n = cut ? it.slots - p.recent : it.slots;  // slots that compete
+  const int want = cut ? p.keep - p.recent : n;
+  for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+  __syncthreads();
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  if (it.slots <= p.keep) {
-    for (int i = tid; i < p.keep; i += kThreads) kept[i] = i < it.slots ? i : -1;
-  } else {
-    const int n = it.slots - p.recent, want = p.keep - p.recent;
-    for (int i = tid; i < p.recent; i += kThreads) kept[want + i] = n + i;
-    if (HELD)
-      for (int i = tid; i < n; i += kThreads) held[i] = order_key(acc[i]);
-    const auto key_at = [&](int i) { return HELD ? held[i] : order_key(acc[i]); };
-    if (want > 0) {
-      uint32_t prefix = 0, mask = 0;
-      int above = 0;
-      for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const int bins = pass == 2 ? 1024 : 2048;
-        for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-          const uint32_t k = key_at(i);
-          if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {  // from the largest bin down, bins / 32 per lane
-          const int span = bins / 32, top = bins - 1 - span * lane;
-          int sum = 0;
-          for (int i = 0; i < span; ++i) sum += hist[top - i];
-          int incl = sum;
+  if (HELD) {  // one read of the weights, with the first digit's histogram
+    constexpr int kPer = 8;
+    for (int i0 = 0; i0 < it.slots; i0 += kPer * kThreads) {
+      float x[kPer];
 #pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += x;
-          }
-          int run = above + incl - sum;
-          if (run < want && above + incl >= want)
-            for (int i = 0; i < span; ++i) {
-              const int c = hist[top - i];
-              if (run + c >= want) {
-                pick[0] = top - i;
-                pick[1] = run;
-                break;
-              }
-              run += c;
-            }
-        }
-        __syncthreads();
-        prefix |= (uint32_t)pick[0] << shift;
-        mask |= (uint32_t)(bins - 1) << shift;
-        above = pick[1];
-      }
-      // Each warp writes the kept slots of one contiguous range, after those of the warps
-      // before it.
-      const int ties = want - above;
-      const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
-      const int a = min(warp * per, n), b = min(a + per, n);
-      int gt = 0, eq = 0;
-      for (int i = a + lane; i < b; i += 32) {
-        const uint32_t k = key_at(i);
-        gt += k > prefix;
-        eq += k == prefix;
+      for (int j = 0; j < kPer; ++j) {
+        const int i = i0 + j * kThreads + tid;
+        x[j] = i < it.slots ? acc[i] : 0.f;
       }
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        gt += __shfl_xor_sync(0xffffffffu, gt, off);
-        eq += __shfl_xor_sync(0xffffffffu, eq, off);
-      }
-      if (lane == 0) {
-        warp_n[warp][0] = gt;
-        warp_n[warp][1] = eq;
-      }
-      __syncthreads();
-      gt = eq = 0;
-      for (int w = 0; w < warp; ++w) {
-        gt += warp_n[w][0];
-        eq += warp_n[w][1];
-      }
-      const uint32_t below = (1u << lane) - 1;
-      for (int i0 = a; i0 < b; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < b ? key_at(i) : 0;
-        const bool is_gt = i < b && k > prefix, is_eq = i < b && k == prefix;
-        const uint32_t bg = __ballot_sync(0xffffffffu, is_gt);
-        const uint32_t be = __ballot_sync(0xffffffffu, is_eq);
-        const int ng = gt + __popc(bg & below), ne = eq + __popc(be & below);
-        if (is_gt || (is_eq && ne < ties)) kept[ng + min(ne, ties)] = i;
-        gt += __popc(bg);
-        eq += __popc(be);
+      for (int j = 0; j < kPer; ++j) {
+        const int i = i0 + j * kThreads + tid;
+        if (i < it.slots) held[i] = x[j];
+        if (cut && i < n) atomicAdd(&hist[order_key(x[j]) >> 21], 1);
       }
     }
   }
-  if (!it.acc_out) return;
+  const auto key_at = [&](int i) { return order_key(HELD ? held[i] : acc[i]); };
+  uint32_t prefix = 0;  // keys above it are kept, and the first `ties` at it
+  int ties = n;         // a row that keeps everything: every key is at or above 0
+  if (cut && want > 0) {
+    uint32_t mask = 0;
+    int above = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = pass == 2 ? 1023 : 2047;
+      if (pass > 0) {
+        for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+        __syncthreads();
+      }
+      if (!HELD || pass > 0)
+        for (int i = tid; i < n; i += kThreads) {
+          const uint32_t k = key_at(i);
+          if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1);
+        }
+      __syncthreads();
+      // Bins from the largest down, two per thread; each warp scans its 64, then adds the
+      // totals of the warps before it.
+      const int top = kBins - 1 - 2 * tid;
+      const int c0 = hist[top], c1 = hist[top - 1];
+      int incl = c0 + c1;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+      }
+      if (lane == 31) warp_n[warp][0] = incl;
+      __syncthreads();
+      int before = lane < warp ? warp_n[lane][0] : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+      const int run = above + before + incl - c0 - c1;  // keys above this thread's bins
+      if (run < want && run + c0 >= want) {
+        pick[0] = top;
+        pick[1] = run;
+        pick[2] = c0;
+      } else if (run + c0 < want && run + c0 + c1 >= want) {
+        pick[0] = top - 1;
+        pick[1] = run + c0;
+        pick[2] = c1;
+      }
+      __syncthreads();
+      prefix |= (uint32_t)pick[0] << shift;
+      mask |= digit << shift;
+      above = pick[1];
+      ties = want - above;
+      if (pick[2] == ties && prefix > 0) {  // every key from the prefix on: no more digits
+        prefix -= 1;
+        ties = 0;
+        break;
+      }
+    }
+  }
+  if (want > 0) {
+    // Each warp writes the kept slots of one contiguous range, after those of the warps
+    // before it.
+    const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int a = min(warp * per, n), b = min(a + per, n);
+    int gt = 0, eq = 0;
+    for (int i = a + lane; i < b; i += 32) {
+      const uint32_t k = key_at(i);
+      gt += k > prefix;
+      eq += k == prefix;
+    }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      gt += __shfl_xor_sync(0xffffffffu, gt, off);
+      eq += __shfl_xor_sync(0xffffffffu, eq, off);
+    }
+    __syncthreads();  // warp_n of the last digit has been read
+    if (lane == 0) {
+      warp_n[warp][0] = gt;
+      warp_n[warp][1] = eq;
+    }
+    __syncthreads();
+    gt = eq = 0;
+    for (int w = 0; w < warp; ++w) {
+      gt += warp_n[w][0];
+      eq += warp_n[w][1];
+    }
+    const uint32_t below = (1u << lane) - 1;
+    for (int i0 = a; i0 < b; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t k = i < b ? key_at(i) : 0;
+      const bool is_gt = i < b && k > prefix, is_eq = i < b && k == prefix;
+      const uint32_t bg = __ballot_sync(0xffffffffu, is_gt);
+      const uint32_t be = __ballot_sync(0xffffffffu, is_eq);
+      const int ng = gt + __popc(bg & below), ne = eq + __popc(be & below);
+      if (is_gt || (is_eq && ne < ties)) {
+        const int at = ng + min(ne, ties);
+        kept[at] = i;
+        if (HELD && out) out[at] = held[i];
+      }
+      gt += __popc(bg);
+      eq += __popc(be);
+    }
+  }
+  if (cut) {
+    for (int i = tid; i < p.recent; i += kThreads) {
+      kept[want + i] = n + i;
+      if (HELD && out) out[want + i] = held[n + i];
+    }
+  } else {
+    for (int i = it.slots + tid; i < p.keep; i += kThreads) kept[i] = -1;
+  }
+  if (HELD || !out) return;
   // The kept accumulators, moved together.  acc_out may be acc_in: a kept slot never lies
   // below its destination, so what a pass writes has been read by it or an earlier one.
-  float *out = it.acc_out + (int64_t)g * p.acc_out_stride;
+  const int m = min(it.slots, p.keep);
   __syncthreads();
   for (int i0 = 0; i0 < m; i0 += kThreads) {
     const int i = i0 + tid;

@@ -1894,11 +1894,11 @@ int flush_copies(CopyParams &cp, cudaStream_t s) {
 // a block-table entry -- so the pieces are independent).
 constexpr int kCopySpan = 2048;
 
-int add_copy(CopyParams &cp, const CopyItem &it, cudaStream_t s) {
-  for (int p = it.p0; p < it.p1; p += kCopySpan) {
+int add_copy(CopyParams &cp, const CopyItem &it, cudaStream_t s, int span = kCopySpan) {
+  for (int p = it.p0; p < it.p1; p += span) {
     CopyItem piece = it;
     piece.p0 = p;
-    piece.p1 = std::min(it.p1, p + kCopySpan);
+    piece.p1 = std::min(it.p1, p + span);
     cp.items[cp.n_items++] = piece;
     if (cp.n_items == kMaxCopyItems) {
       const int rc = flush_copies(cp, s);
@@ -2740,6 +2740,14 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
 }  // extern "C"
 
 // ---------------------------------------------------------------- eviction
+namespace {
+
+// Positions per copy item of the rings of evicted rows: a ring is short, and a CTA walks its
+// item (32 rows x 8 heads x 512 positions, D = 128: 25.8 us in whole rings).
+constexpr int kRingSpan = 128;
+
+}  // namespace
+
 extern "C" {
 
 int kv_get_slots(const kv_cache *c, int32_t *slots_out) {
@@ -2924,7 +2932,7 @@ int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
       it.src_ring = src->R;
       it.dst_ring = dst->R;
       it.src_base = it.dst_base = 0;
-      if (add_copy(cp, it, s) != KV_OK) return KV_ERR_CUDA;
+      if (add_copy(cp, it, s, kRingSpan) != KV_OK) return KV_ERR_CUDA;
     }
   }
   if (cp.n_items && flush_copies(cp, s) != KV_OK) return KV_ERR_CUDA;
