@@ -160,6 +160,14 @@ __global__ void __launch_bounds__(128) state_kernel(const __grid_constant__ Stat
   ptx::grid_dep_launch();
   const int r = blockIdx.x;
   const int b = p.cache_row[r];
+  if (p.reset == 2) {  // slot s: the largest position below n that is s modulo R, if any
+    const int n = p.n[r], base = n > 0 ? (n - 1) / p.ring_R * p.ring_R : 0;
+    for (int s = threadIdx.x; s < p.ring_R; s += blockDim.x) {
+      const int pos = base + s < n ? base + s : base + s - p.ring_R;
+      p.lpos[(int64_t)b * p.ring_R + s] = pos >= 0 ? pos : -1;
+    }
+    return;
+  }
   if (p.reset) {
     for (int s = threadIdx.x; s < p.ring_R; s += blockDim.x) p.lpos[(int64_t)b * p.ring_R + s] = -1;
     return;

@@ -270,7 +270,8 @@ struct CommitParams {
 struct StateParams {
   int32_t *lpos;       // [B][R]
   int ring_R, window;
-  int reset;           // 1: lpos = -1; 0: record the kept positions of the advance
+  int reset;           // 1: lpos = -1; 0: record the kept positions of the advance; 2: the
+                       // whole ring of a row that holds positions [0, n)
   int n_rows;
   int32_t cache_row[kMaxRowsPerLaunch];
   int32_t lens[kMaxRowsPerLaunch];   // lens before the advance
@@ -296,6 +297,11 @@ constexpr int kMaxCopyItems = 256;
 struct CopyParams {
   int Hk, D;
   int n_items;
+  // 1: a programmatic launch that runs beside the launch before it, which neither writes
+  // what the copies read nor reads or writes what they write; its first CTA waits for that
+  // launch at its end, so that this one's completion still means that all before it have
+  // completed.  The launch before must let it start only after its own grid wait.
+  int beside;
   CopyItem items[kMaxCopyItems];
 };
 
@@ -423,7 +429,6 @@ struct EvictItem {
   __nv_bfloat16 *dst_k, *dst_v;
   int32_t src_row, dst_row;
   int32_t slots;         // the source row's keys
-  int32_t in_place;      // the destination is the source row itself
 };
 constexpr int kMaxEvictItems = 256;
 struct EvictParams {
@@ -462,7 +467,7 @@ cudaError_t launch_k(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cuda
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-cudaError_t launch_copy(const CopyParams &p, cudaStream_t s);
+cudaError_t launch_copy(const CopyParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_table(const TableParams &p, cudaStream_t s);
 // Split-K schedule of one decode launch over p.rows[0, n) (n <= kMaxRowsPerLaunch), whose
 // cache_row, call_row, pos, nk and ctr the caller has set: row i reads nk slots of segment

@@ -7,6 +7,7 @@
 // if they were positions ("inkling: ring-buffer KV cache for sliding-window layers",
 // review: grow-with-copy keeps `t % win` valid only when the ring is copied by position).
 #include "kvinc_internal.h"
+#include "ptx.cuh"
 
 namespace kvinc {
 namespace {
@@ -23,6 +24,7 @@ __device__ __forceinline__ int64_t elem_of(int p, int h, int D, const int32_t *t
 // most 2048 positions; 16-byte chunks of K and V, every load of a pass issued before the
 // first store.
 __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ CopyParams p) {
+  if (p.beside) ptx::grid_dep_launch();
   const CopyItem &it = p.items[blockIdx.x];
   const int h = blockIdx.y;
   const int vec = p.D / 8;
@@ -57,14 +59,14 @@ __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ CopyP
       *reinterpret_cast<uint4 *>(dv + d) = vv[i];
     }
   }
+  if (p.beside && blockIdx.x == 0 && blockIdx.y == 0) ptx::grid_dep_wait();
 }
 
 }  // namespace
 
-cudaError_t launch_copy(const CopyParams &p, cudaStream_t s) {
+cudaError_t launch_copy(const CopyParams &p, cudaStream_t s, bool pdl) {
   if (p.n_items <= 0) return cudaSuccess;
-  copy_kernel<<<dim3(p.n_items, p.Hk), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_k(copy_kernel, dim3(p.n_items, p.Hk), dim3(256), 0, s, p, pdl);
 }
 
 }  // namespace kvinc
