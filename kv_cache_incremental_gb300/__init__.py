@@ -70,11 +70,31 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-class _DevArray:
-    """Zero-copy __cuda_array_interface__ view of library-owned device memory; holds the cache
-    that owns it, and a tensor made from it holds the view, so the memory outlives both."""
+class _Handle:
+    """A kv_cache of the library; destroyed by close(), or with the last reference: the
+    KVCache's or a view's."""
 
-    def __init__(self, ptr: int, shape, typestr: str, owner: "KVCache"):
+    def __init__(self, h):
+        self.h = h
+
+    def close(self) -> None:
+        if self.h:
+            _clib.kv_cache_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class _DevArray:
+    """Zero-copy __cuda_array_interface__ view of library-owned device memory; holds the
+    handle that owns it, and a tensor made from it holds the view, so the memory outlives
+    both."""
+
+    def __init__(self, ptr: int, shape, typestr: str, owner: _Handle):
         self.owner = owner
         self.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": typestr,
                                          "data": (ptr, False), "version": 3, "strides": None}
@@ -100,6 +120,8 @@ class KVCache:
                                              int(paged_blocks)), "kv_cache_create_paged")
         self.paged_blocks = paged_blocks
         self._h = h
+        self._owner = _Handle(h)
+        self._views = {}  # layer -> (K, V) views of dense storage, made on first use
         self.B, self.max_len, self.Hq, self.Hk, self.D, self.W = B, max_len, Hq, Hk, D, W
         self.layer_kinds = list(layer_kinds)
         self.device = device
@@ -114,14 +136,9 @@ class KVCache:
         for g in list(getattr(self, "_graphs", ())):
             g.close()
         if getattr(self, "_h", None):
-            _clib.kv_cache_destroy(self._h)
+            self._views.clear()
+            self._owner.close()
             self._h = None
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
 
     # ------------------------------------------------------------------ checks
     def _check_tensor(self, x, name, heads, C=None, Bs=None):
@@ -142,8 +159,8 @@ class KVCache:
             raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
         if not x.is_cuda or x.device.index != self.device:
             raise ValueError(f"{name} must live on cuda:{self.device}")
-        if tuple(x.shape) != tuple(shape):
-            raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(x.shape)}")
+        if x.shape != shape:
+            raise ValueError(f"{name}: expected {shape}, got {tuple(x.shape)}")
         if not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
@@ -274,23 +291,26 @@ class KVCache:
                 kept = [torch.empty((n, self.Hk, max(keep, 0)), dtype=torch.int32,
                                     device=f"cuda:{self.device}") if kind == KV_GLOBAL else None
                         for kind in self.layer_kinds]
-        lists = [acc, [None] * L if acc_out is None else acc_out, kept]
+        ptrs = []
         for xs, name, dtype, shape in (
-                (lists[0], "acc", torch.float32, (src.B, src.Hk, src.max_len)),
-                (lists[1], "acc_out", torch.float32, (self.B, self.Hk, self.max_len)),
-                (lists[2], "kept", torch.int32, (n, self.Hk, keep))):
+                (acc, "acc", torch.float32, (src.B, src.Hk, src.max_len)),
+                (acc_out, "acc_out", torch.float32, (self.B, self.Hk, self.max_len)),
+                (kept, "kept", torch.int32, (n, self.Hk, keep))):
+            ps = (ctypes.c_void_p * L)()
+            ptrs.append(ps)
+            if xs is None and name == "acc_out":
+                continue
             if len(xs) != L:
                 raise ValueError(f"{name}: one entry per layer ({L})")
             for l, x in enumerate(xs):
-                if x is None and self.layer_kinds[l] == KV_GLOBAL and name != "acc_out":
-                    raise ValueError(f"{name}[{l}]: a global layer needs a tensor")
                 if x is not None:
-                    self._check_plain(x, f"{name}[{l}]", dtype, shape)
-        ptrs = [(ctypes.c_void_p * L)(*[None if x is None else x.data_ptr() for x in xs])
-                for xs in lists]
-        check(_clib.kv_evict_rows(self._h, _i32_array(dst_rows), src._h, _i32_array(src_rows), n,
-                                 keep, recent, *ptrs, _stream_ptr(stream, self.device)),
-              "kv_evict_rows")
+                    self._check_plain(x, name, dtype, shape)
+                    ps[l] = x.data_ptr()
+                elif self.layer_kinds[l] == KV_GLOBAL and name != "acc_out":
+                    raise ValueError(f"{name}[{l}]: a global layer needs a tensor")
+        check(_clib.kv_evict_rows(self._h, self._memo_n.get(dst_rows), src._h,
+                                 self._memo_rows.get(src_rows), n, keep, recent, *ptrs,
+                                 _stream_ptr(stream, self.device)), "kv_evict_rows")
         return kept
 
     def evict(self, rows, keep: int, recent: int, acc, kept=None, stream=None):
@@ -303,10 +323,9 @@ class KVCache:
         import torch
         kp, vp = ctypes.c_void_p(), ctypes.c_void_p()
         check(_clib.kv_debug_ring_ptrs(self._h, layer, ctypes.byref(kp), ctypes.byref(vp)))
-        dev = f"cuda:{self.device}"
         shape = (self.B, self.Hk, self.R + 1, self.D)
-        K = torch.as_tensor(_DevArray(kp.value, shape, "<i2", self), device=dev).view(torch.bfloat16)
-        V = torch.as_tensor(_DevArray(vp.value, shape, "<i2", self), device=dev).view(torch.bfloat16)
+        K = self._bf16_view(kp, shape)
+        V = self._bf16_view(vp, shape)
         return K, V
 
     def copy_rows(self, src: "KVCache", src_rows, dst_rows, keep=None, stream=None) -> None:
@@ -418,21 +437,29 @@ class KVCache:
     def nbytes(self) -> int:
         return int(_clib.kv_nbytes(self._h))
 
+    def _bf16_view(self, ptr, shape):
+        import torch
+        return torch.as_tensor(_DevArray(ptr.value, shape, "<i2", self._owner),
+                               device=f"cuda:{self.device}").view(torch.bfloat16)
+
     def storage(self, layer: int):
         """Torch views (K, V) of a layer's storage, [B, Hk, rows, D] bf16; rows = max_len + 1
         (global, and a hybrid layer's group cache) or R + 1 (sliding).  Zero-copy, valid until
-        the cache is closed (a view keeps it from being collected), except for a paged cache's global layers: there each row's
-        blocks are gathered from the pool into a new tensor (slots past the row's blocks are
-        zero)."""
+        the cache is closed (a view keeps its memory when the cache itself is dropped), except
+        for a paged cache's global layers: there each row's blocks are gathered from the pool
+        into a new tensor (slots past the row's blocks are zero)."""
         import torch
+        views = self._views.get(layer)
+        if views is not None:
+            return views[0].detach(), views[1].detach()
         kp, vp, lp = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_void_p()
         check(_clib.kv_debug_ptrs(self._h, layer, ctypes.byref(kp), ctypes.byref(vp),
                                  ctypes.byref(lp)))
         dev = f"cuda:{self.device}"
         if self.paged_blocks is not None and self.layer_kinds[layer] != KV_SLIDING:
             pool = (self.Hk, self.paged_blocks, 16, self.D)   # head-major pool
-            Kp = torch.as_tensor(_DevArray(kp.value, pool, "<i2", self), device=dev).view(torch.bfloat16)
-            Vp = torch.as_tensor(_DevArray(vp.value, pool, "<i2", self), device=dev).view(torch.bfloat16)
+            Kp = self._bf16_view(kp, pool)
+            Vp = self._bf16_view(vp, pool)
             Kp, Vp = Kp.transpose(0, 1), Vp.transpose(0, 1)  # [block][Hk][16][D]
             shape = (self.B, self.Hk, self.max_len + 1, self.D)
             K = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
@@ -448,9 +475,10 @@ class KVCache:
             return K, V
         rows = self.R + 1 if self.layer_kinds[layer] == KV_SLIDING else self.max_len + 1
         shape = (self.B, self.Hk, rows, self.D)
-        K = torch.as_tensor(_DevArray(kp.value, shape, "<i2", self), device=dev).view(torch.bfloat16)
-        V = torch.as_tensor(_DevArray(vp.value, shape, "<i2", self), device=dev).view(torch.bfloat16)
-        return K, V
+        K = self._bf16_view(kp, shape)
+        V = self._bf16_view(vp, shape)
+        self._views[layer] = (K, V)
+        return K.detach(), V.detach()
 
     def block_table(self, row: int):
         """Pool blocks of a row in position order (paged caches; [] otherwise)."""
@@ -471,7 +499,7 @@ class KVCache:
         check(_clib.kv_debug_ptrs(self._h, 0, None, None, ctypes.byref(lp)))
         if not lp.value:
             return None
-        return torch.as_tensor(_DevArray(lp.value, (self.B, self.R), "<i4", self),
+        return torch.as_tensor(_DevArray(lp.value, (self.B, self.R), "<i4", self._owner),
                                device=f"cuda:{self.device}")
 
     def debug_wait_timeout(self, limit: int = 4096, stream=None) -> None:

@@ -1,21 +1,47 @@
-"""Zero-copy views of a cache's storage keep the cache, and so the memory, alive."""
+"""Zero-copy views of a cache's storage keep its memory when the cache itself is dropped."""
 import gc
-import weakref
 
 import pytest
 
 pytestmark = pytest.mark.gpu
 
 
-def test_views_keep_the_cache_alive():
+def free_bytes():
+    import torch
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()      # what torch itself holds but does not use
+    return torch.cuda.mem_get_info()[0]
+
+
+def test_views_keep_the_memory_alive():
+    import torch
     import kv_cache_incremental_gb300 as kvi
-    c = kvi.KVCache(2, 64, 4, 2, 64, 8, [0, 1])
-    ref = weakref.ref(c)
+    torch.zeros(1, device="cuda")
+    kvi.KVCache(1, 8, 4, 2, 64).close()                   # contexts, modules
+    before = free_bytes()
+    c = kvi.KVCache(8, 4096, 4, 4, 128, 8, [0, 1])        # 64 MiB of keys and values
     views = [*c.storage(0), *c.storage(1), c.lpos()]
-    del c
+    again = c.storage(0)
+    assert again[0].data_ptr() == views[0].data_ptr() and again[0] is not views[0]
+    held = free_bytes()
+    assert before - held > 60 << 20
+    del c, again
     gc.collect()
-    assert ref() is not None
+    assert free_bytes() <= held + (1 << 20)               # not freed under the views
     assert all(float(v.float().abs().max()) <= 1 for v in views)    # zeros, and -1 in lpos
     del views
     gc.collect()
-    assert ref() is None
+    assert free_bytes() - held > 60 << 20
+
+
+def test_close_frees_at_once_and_twice_is_fine():
+    import torch
+    import kv_cache_incremental_gb300 as kvi
+    torch.zeros(1, device="cuda")
+    c = kvi.KVCache(8, 4096, 4, 4, 128)
+    view = c.storage(0)
+    held = free_bytes()
+    c.close()
+    c.close()
+    assert free_bytes() - held > 60 << 20
+    del view, c
