@@ -42,6 +42,8 @@
  *    that is itself launched programmatically after a library call must wait
  *    for its predecessor (griddepcontrol.wait) before reading the call's output,
  *    as with any programmatic launch.
+ *  - A call captured into a CUDA graph replays with the rows and lengths of the moment it was
+ *    captured; the host's side of it (lengths, block tables) is done once, at the capture.
  *  - Not thread-safe: one cache is driven from one host thread and one
  *    stream at a time.
  *  - Tensors are bfloat16, row-major, contiguous, 16-byte aligned.

@@ -72,12 +72,15 @@ def _stream_ptr(stream, device):
 
 class _Handle:
     """A kv_cache of the library; destroyed by close(), or with the last reference: the
-    KVCache's or a view's."""
+    KVCache's or a view's.  Step graphs over it that still live are destroyed before it, in
+    whatever order the collector finalises them."""
 
     def __init__(self, h):
-        self.h = h
+        self.h, self.graphs = h, set()
 
     def close(self) -> None:
+        for g in list(self.graphs):
+            g.close()
         if self.h:
             _clib.kv_cache_destroy(self.h)
             self.h = None
@@ -87,6 +90,20 @@ class _Handle:
             self.close()
         except Exception:
             pass
+
+
+class _GraphHandle:
+    """A kv_step_graph of the library, over the cache of `owner`."""
+
+    def __init__(self, h, owner: _Handle):
+        self.h, self.owner = h, owner
+        owner.graphs.add(self)
+
+    def close(self) -> None:
+        if self.h:
+            _clib.kv_step_graph_destroy(self.h)
+            self.h = None
+            self.owner.graphs.discard(self)
 
 
 class _DevArray:
@@ -553,6 +570,7 @@ class StepGraph:
                                             *self._ptrs(q, k, v, out), cache.Hq,
                                             _i32_array(rows), Bs), "kv_step_graph_create")
         self._h, self.cache, self.Bs = h, cache, Bs
+        self._graph = _GraphHandle(h, cache._owner)
         # the graph reads these buffers
         self._keep = (list(q), list(k), list(v), list(out), k_global, v_global)
         cache._graphs.add(self)
@@ -620,7 +638,7 @@ class StepGraph:
 
     def close(self) -> None:
         if getattr(self, "_h", None):
-            _clib.kv_step_graph_destroy(self._h)
+            self._graph.close()
             self._h = None
 
     def __del__(self):

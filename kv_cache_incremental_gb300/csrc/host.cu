@@ -2224,6 +2224,17 @@ int kv_import_row(kv_cache *c, int row, int keep, const void *src, int64_t bytes
 // ---------------------------------------------------------------- sparse attention
 namespace {
 
+// A call that is being captured runs when its graph is replayed, not now: what it would leave
+// behind is not known yet.
+bool is_capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+    cudaGetLastError();
+    return true;
+  }
+  return st != cudaStreamCaptureStatusNone;
+}
+
 // Bounds of the complete blocks of `rows` that have none yet, where row i has `slots[i]`
 // slots filled.  Only blocks below `kept[i]` slots stay known: the slots above are of
 // tokens that a later call of the same step may write again.
@@ -2257,6 +2268,7 @@ int update_bounds(kv_cache *c, int layer, const std::vector<int32_t> &rows,
     if (bp.n_rows == kMaxRowsPerLaunch && flush() != KV_OK) return KV_ERR_CUDA;
   }
   if (bp.n_rows > 0 && flush() != KV_OK) return KV_ERR_CUDA;
+  if (is_capturing(s)) return KV_OK;
   for (size_t i = 0; i < rows.size(); ++i)
     valid[rows[i]] = std::max(valid[rows[i]], kept[i] / kSparseBlock);
   return KV_OK;
@@ -2452,7 +2464,7 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
   // Calls of single-token rows append (and bound a row's one or two pending blocks) in the
   // selection's launch; the others, and rows behind by more blocks, in launches before it.
   std::vector<int32_t> &valid = c->sparse.valid[layer];
-  const bool fused = max_n == 1;
+  const bool fused = max_n == 1, capturing = is_capturing(s);
   if (fused) {
     std::vector<int32_t> far, far_slots;
     for (size_t i = 0; i < live.size(); ++i)
@@ -2494,9 +2506,9 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
       }
       SelectQuery sq = {r, slot, c->lens[r] + t, tok, 0, 0};
       if (fused) {  // blocks complete with this token; known from now on up to the cached ones
-        sq.pend0 = valid[r];
-        sq.n_pend = std::max(0, (slot + 1) / kSparseBlock - valid[r]);
-        valid[r] = std::max(valid[r], slot / kSparseBlock);
+        sq.pend0 = slot / kSparseBlock - valid[r] > 1 ? slot / kSparseBlock : valid[r];
+        sq.n_pend = std::max(0, (slot + 1) / kSparseBlock - sq.pend0);
+        if (!capturing) valid[r] = std::max(valid[r], slot / kSparseBlock);
       }
       batch.push_back(sq);
     }
@@ -2803,21 +2815,27 @@ int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
   // row lets go of its blocks and takes fresh ones.
   const bool paged = dst->n_blocks > 0;
   if (paged) {
-    std::unordered_map<int32_t, int32_t> drops;
-    int64_t take = 0;
+    std::unordered_map<int32_t, int32_t> refs;  // of the blocks whose holders change
+    const auto ref = [&](int b) -> int32_t & {
+      return refs.emplace(b, dst->refs[b]).first->second;
+    };
+    int64_t avail = (int64_t)dst->free_blocks.size();
+    for (int i = 0; i < n; ++i)
+      if (!in_place(i))
+        for (int b : dst->rblocks[dst_rows[i]]) avail += --ref(b) == 0;
     for (int i = 0; i < n; ++i) {
-      const auto &rb = dst->rblocks[dst_rows[i]];
-      if (in_place(i)) {
-        if (slots[i] <= keep) continue;
-        for (int x = 0; x < blocks_for(m[i]); ++x) take += dst->refs[rb[x]] > 1;
-      } else {
-        take += blocks_for(m[i]);
-        for (int b : rb) ++drops[b];
+      if (!in_place(i)) {
+        avail -= blocks_for(m[i]);
+      } else if (slots[i] > keep) {
+        const auto &rb = dst->rblocks[dst_rows[i]];
+        for (int x = 0; x < blocks_for(m[i]); ++x)
+          if (ref(rb[x]) > 1) {
+            --ref(rb[x]);
+            --avail;
+          }
       }
     }
-    int64_t freed = 0;
-    for (const auto &e : drops) freed += dst->refs[e.first] == e.second;
-    if (take > (int64_t)dst->free_blocks.size() + freed) return KV_ERR_POOL;
+    if (avail < 0) return KV_ERR_POOL;
     static thread_local TableParams tp;
     static thread_local CopyParams cp;
     tp.table = dst->table;

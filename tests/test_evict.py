@@ -332,6 +332,41 @@ def graph_step(r):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_step_graph_made_before_the_eviction(paged):
+    import torch
+    r = Rows(3, 400, 8, 2, 64, [300, 90, 17], seed=13, paged=paged)
+    q, k, v = r.tokens(3, 1)
+    qd, kd, vd = dev(q), dev(k), dev(v)
+    out = torch.empty_like(qd)
+    g = r.cache.step_graph([qd], [kd], [vd], [out])
+    for keep in (None, 64, 40):
+        if keep:
+            evict(r, r, [0, 1], [0, 1], keep, 9)
+        q, k, v = r.tokens(3, 1)
+        qd.copy_(dev(q)), kd.copy_(dev(k)), vd.copy_(dev(v))
+        out.fill_(12345.0)
+        g.launch()
+        torch.cuda.synchronize()
+        check_dense(r, [1] * 3, q, k, v, bits_of(out))
+    check_state(r)
+    g.close()
+
+
+@pytest.mark.gpu
+def test_shared_blocks_are_counted_once():
+    """Two rows cut in place that hold the same blocks: one of them keeps the originals, so
+    copies for the other are all the pool has to give."""
+    r = Rows(2, 64, 4, 2, 64, [48, 0], seed=14, paged=True, blocks=5)
+    r.cache.copy_rows(r.cache, [0], [1])
+    r.K[0][1], r.V[0][1], r.lens[1] = r.K[0][0], r.V[0][0], 48
+    assert r.cache.free_blocks == 2
+    evict(r, r, [0, 1], [0, 1], 32, 3)
+    check_state(r)
+    assert r.cache.free_blocks == 1
+
+
+@pytest.mark.gpu
 def test_sliding_and_global_layers_keep_their_own_positions():
     """Two layers: after an eviction the sliding one still goes by positions (ring slots,
     window, rotation), the global one by slots."""

@@ -297,6 +297,34 @@ def test_other_stream_and_a_captured_call():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("behind", [64, 400])
+def test_a_captured_call_that_never_ran_leaves_no_bounds_behind(behind):
+    """Bounds that a captured call would compute count only once they have been computed."""
+    import torch
+    r = Rows(2, 900, 8, 2, 64, [700, 128 + 63], seed=43)
+    r.cache.enable_sparse(4)
+    q, k, v = r.tokens(2, 1)
+    qd, kd, vd = dev(q), dev(k), dev(v)
+    # warm up on another cache, so that nothing is computed here before the capture
+    w = Rows(2, 900, 8, 2, 64, [700, 128 + 63], seed=43)
+    w.cache.enable_sparse(4)
+    out = torch.empty_like(qd)
+    w.cache.append_sparse(0, qd, kd, vd, [1, 1], 1, sink=0, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r.cache.append_sparse(0, qd, kd, vd, [1, 1], 1, sink=0, out=out)
+    if behind == 64:
+        chunk = r.tokens(2, 2)
+        step(r, [1, 1], 0, 1, 2, qkv=(q, k, v))
+        step(r, [2, 2], 0, 1, 2, qkv=chunk)
+    else:
+        step(r, [70, 2], 0, 1, 2)
+        step(r, [1, 1], 0, 1, 2)
+    del g
+
+
+@pytest.mark.gpu
 def test_refusals_change_nothing():
     import torch
     import kv_cache_incremental_gb300 as kvi

@@ -45,3 +45,22 @@ def test_close_frees_at_once_and_twice_is_fine():
     c.close()
     assert free_bytes() - held > 60 << 20
     del view, c
+
+
+def test_a_cache_and_its_graph_collected_together():
+    """A reference cycle that holds a cache, a view and a step graph: the collector may
+    finalise them in any order."""
+    import torch
+    import kv_cache_incremental_gb300 as kvi
+    torch.zeros(1, device="cuda")
+    before = free_bytes()
+    for _ in range(3):
+        c = kvi.KVCache(8, 4096, 4, 4, 128)
+        q = torch.zeros((8, 1, 4, 128), dtype=torch.bfloat16, device="cuda")
+        ring = [c.step_graph([q], [q], [q], [q.clone()]), c, c.storage(0)]
+        ring.append(ring)
+        ring[0].launch()
+        torch.cuda.synchronize()
+        del c, q, ring
+        gc.collect()
+    assert before - free_bytes() < 40 << 20
