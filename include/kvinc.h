@@ -106,10 +106,12 @@ enum kv_status {
  * and V, the RoPE table [max_len][D/2] of (cos, sin) float pairs computed on
  * the host in double, decode split-K partials (min(B, 512) x 32 x Hq vectors of
  * D floats) and chunked-prefill key-split partials (min(1024 x SMs,
- * B x Hq x 64 x 16) vectors of D floats).  Every later call works within this
+ * B x Hq x 64 x 16) vectors of D floats, or, with a global layer, room for the scores of
+ * kv_append_weights where that is more: B x Hq x max_len floats, at most 2048 x SMs
+ * vectors).  Every later call works within this
  * memory: none allocates device memory except kv_append_host / kv_append_hybrid_host
- * with pageable buffers (their staging) and kv_step_graph_create (the graph's own
- * resources, at instantiation).  All lens start at 0.
+ * with pageable buffers (their staging), kv_step_graph_create (the graph's own
+ * resources, at instantiation) and kv_sparse_enable.  All lens start at 0.
  * On success *out holds the cache; on failure *out is NULL.
  */
 int kv_cache_create(kv_cache **out, int B, int max_len, int Hq, int Hk, int D, int W,

@@ -610,6 +610,14 @@ int64_t prefill_part_reserve(int num_sms, int B, int Hq) {
   return std::min<int64_t>(prefill_part_cap(num_sms),
                            (int64_t)B * Hq * kChunk * kMaxPrefillSplits);
 }
+// The same memory, in vectors of D floats, holds the scores of an accumulating decode call
+// (kv_append_weights): one float per row, query head and slot, up to twice the prefill bound.
+// With the prefill bound alone 16 rows of 16k-32k keys at Hq = 64 took two launches and 329
+// us, with this one launch and 294 us.
+int64_t score_reserve(int num_sms, int B, int Hq, int max_len, int D) {
+  return std::min<int64_t>(2 * prefill_part_cap(num_sms),
+                           ((int64_t)B * Hq * ((int64_t)max_len + 3) + D - 1) / D);
+}
 
 // The prefill entries of one sub-chunk, per launch kind, with their key splits; the
 // merges of the split rows and the partial vectors they need, at most
@@ -1110,6 +1118,9 @@ static int create_impl(kv_cache **out, int B, int max_len, int Hq, int Hk, int D
   // prefill key-split partials: every call's plan fits (plan_prefill), so kv_append never
   // allocates
   c->ppart_cap = prefill_part_reserve(c->num_sms, B, Hq);
+  for (int k : c->kind)
+    if (k == KV_GLOBAL)
+      c->ppart_cap = std::max(c->ppart_cap, score_reserve(c->num_sms, B, Hq, max_len, D));
   if (!alloc((void **)&c->ppart_o, (size_t)c->ppart_cap * D * 4) ||
       !alloc((void **)&c->ppart_ml, (size_t)c->ppart_cap * 8))
     return fail(KV_ERR_OOM);
