@@ -101,7 +101,11 @@ struct WarpAcc {
 // whose 128-byte panels are `pstride` bytes apart.  Keys r < n_valid, r != skip are
 // visible; the V rows of the others must already be zero.
 // SCORES: the visible keys' scores go to scores[h * score_stride + key], h < rep.
-template <int D, int NT, bool SCORES>
+// LAZY: the running maximum moves only when a score exceeds it by kSlack, so that most steps
+// have no exchange between lanes and no rescaling; weights then reach 2^kSlack, which neither
+// their bf16 halves nor the float sums mind.
+constexpr float kSlack = 8.f;
+template <int D, int NT, bool SCORES, bool LAZY>
 __device__ __forceinline__ void attend16(WarpAcc<D, NT> &acc, const uint32_t (&qb)[NT][D / 16][2],
                                          const uint8_t *kt, const uint8_t *vt, int pstride,
                                          int row0, int n_valid, int skip, float scale_log2,
@@ -145,28 +149,61 @@ __device__ __forceinline__ void attend16(WarpAcc<D, NT> &acc, const uint32_t (&q
         if (vb) s1[8] = t3;
       }
     }
-    float mx0 = fmaxf(t0, t2), mx1 = fmaxf(t1, t3);
+    float p0, p1, p2, p3;
+    if (LAZY) {
+      const float g0 = fmaxf(t0, t2), g1 = fmaxf(t1, t3);
+      if (__any_sync(0xffffffffu, g0 > acc.m[nt][0] + kSlack || g1 > acc.m[nt][1] + kSlack)) {
+        float mx0 = g0, mx1 = g1;
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-    }
-    const float mn0 = fmaxf(acc.m[nt][0], mx0), mn1 = fmaxf(acc.m[nt][1], mx1);
-    const float b0 = mn0 == -INFINITY ? 0.f : mn0;
-    const float b1 = mn1 == -INFINITY ? 0.f : mn1;
-    const float al0 = exp2f(acc.m[nt][0] - b0), al1 = exp2f(acc.m[nt][1] - b1);
-    const float p0 = exp2f(t0 - b0), p1 = exp2f(t1 - b1);
-    const float p2 = exp2f(t2 - b0), p3 = exp2f(t3 - b1);
-    acc.m[nt][0] = mn0;
-    acc.m[nt][1] = mn1;
-    acc.l[nt][0] = acc.l[nt][0] * al0 + (p0 + p2);
-    acc.l[nt][1] = acc.l[nt][1] * al1 + (p1 + p3);
+        for (int off = 4; off < 32; off <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+        }
+        const float mn0 = fmaxf(acc.m[nt][0], mx0), mn1 = fmaxf(acc.m[nt][1], mx1);
+        const float al0 = ptx::ex2(acc.m[nt][0] - (mn0 == -INFINITY ? 0.f : mn0));
+        const float al1 = ptx::ex2(acc.m[nt][1] - (mn1 == -INFINITY ? 0.f : mn1));
+        acc.m[nt][0] = mn0;
+        acc.m[nt][1] = mn1;
+        acc.l[nt][0] *= al0;
+        acc.l[nt][1] *= al1;
 #pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt) {
-      acc.o[mt][nt][0] *= al0;
-      acc.o[mt][nt][1] *= al1;
-      acc.o[mt][nt][2] *= al0;
-      acc.o[mt][nt][3] *= al1;
+        for (int mt = 0; mt < D / 16; ++mt) {
+          acc.o[mt][nt][0] *= al0;
+          acc.o[mt][nt][1] *= al1;
+          acc.o[mt][nt][2] *= al0;
+          acc.o[mt][nt][3] *= al1;
+        }
+      }
+      const float b0 = acc.m[nt][0] == -INFINITY ? 0.f : acc.m[nt][0];
+      const float b1 = acc.m[nt][1] == -INFINITY ? 0.f : acc.m[nt][1];
+      p0 = ptx::ex2(t0 - b0), p1 = ptx::ex2(t1 - b1);
+      p2 = ptx::ex2(t2 - b0), p3 = ptx::ex2(t3 - b1);
+      acc.l[nt][0] += p0 + p2;
+      acc.l[nt][1] += p1 + p3;
+    } else {
+      float mx0 = fmaxf(t0, t2), mx1 = fmaxf(t1, t3);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+      }
+      const float mn0 = fmaxf(acc.m[nt][0], mx0), mn1 = fmaxf(acc.m[nt][1], mx1);
+      const float b0 = mn0 == -INFINITY ? 0.f : mn0;
+      const float b1 = mn1 == -INFINITY ? 0.f : mn1;
+      const float al0 = exp2f(acc.m[nt][0] - b0), al1 = exp2f(acc.m[nt][1] - b1);
+      p0 = exp2f(t0 - b0), p1 = exp2f(t1 - b1);
+      p2 = exp2f(t2 - b0), p3 = exp2f(t3 - b1);
+      acc.m[nt][0] = mn0;
+      acc.m[nt][1] = mn1;
+      acc.l[nt][0] = acc.l[nt][0] * al0 + (p0 + p2);
+      acc.l[nt][1] = acc.l[nt][1] * al1 + (p1 + p3);
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        acc.o[mt][nt][0] *= al0;
+        acc.o[mt][nt][1] *= al1;
+        acc.o[mt][nt][2] *= al0;
+        acc.o[mt][nt][3] *= al1;
+      }
     }
     uint32_t h01, l01, h23, l23;
     ptx::split_bf16(p0, p1, h01, l01);
@@ -231,6 +268,7 @@ template <int D, int NT, bool DEEP, int MODE>
 __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
     decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr bool LIST = MODE == kDecodeList, SCORES = MODE == kDecodeScores;
+  constexpr bool LAZY = LIST || SCORES;
   using Cfg = DecodeCfg<D, DEEP>;
   constexpr int kStages = Cfg::kStages;
   constexpr int kHalf = D / 2;
@@ -567,14 +605,14 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     }
-    attend16<D, NT, SCORES>(acc, qb, kt, vt, kTileKeys * 128, 16 * warp, n_valid,
+    attend16<D, NT, SCORES, LAZY>(acc, qb, kt, vt, kTileKeys * 128, 16 * warp, n_valid,
                             skip_here ? skip : -1, p.scale_log2, lane, scores + key_base,
                             p.score_stride, p.rep);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&empty[s]);
   }
   if (owner && warp == 0 && !*fail)  // the new key, from the mini-tile (row 0 only)
-    attend16<D, NT, SCORES>(acc, qb, mini_k, mini_v, kMiniRows * 128, 0, 1, -1, p.scale_log2, lane,
+    attend16<D, NT, SCORES, LAZY>(acc, qb, mini_k, mini_v, kMiniRows * 128, 0, 1, -1, p.scale_log2, lane,
                             scores + new_slot, p.score_stride, p.rep);
 
   // ---------------------------------------------------------------- merge warps
