@@ -54,19 +54,22 @@ constexpr int kMiniRows = 16;  // rows of the new-key mini-tile
 // per SM: more warps to hide the shorter tiles' latency; the continuous-batch mix's decode
 // launches 5.45 -> 5.04 ms over 50 steps against six stages at two CTAs per SM), or with
 // DEEP twice that (one CTA per SM) for launches of at most one wave, whose CTAs each need
-// twice the bytes in flight to keep HBM busy.
-template <int D, bool DEEP>
+// twice the bytes in flight to keep HBM busy.  LIST at D = 64: three stages and four CTAs per
+// SM, since chunks read their blocks from L2 and the CTAs' chains of tiles bound them (24 rows
+// with chunks of up to 64 tokens over 19 blocks, the whole call: 101.7 -> 96.3 us; at D = 128
+// two stages and three CTAs lost, 16 rows over 37 blocks 40.4 -> 42.8).
+template <int D, bool DEEP, bool LIST = false>
 struct DecodeCfg {
   static constexpr int kPanels = D / 64;                        // 128-byte swizzle panels
   static constexpr int kTileBytes = kPanels * kTileKeys * 128;  // one K or V tile
-  static constexpr int kStages = (D == 128 ? 3 : 4) * (DEEP ? 2 : 1);
+  static constexpr int kStages = (D == 128 || LIST ? 3 : 4) * (DEEP ? 2 : 1);
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kMiniBytes = kPanels * kMiniRows * 128;  // one K or V mini-tile
 };
 
-template <int D, int NT, bool DEEP>
+template <int D, int NT, bool DEEP, bool LIST = false>
 constexpr int decode_smem_bytes() {
-  using C = DecodeCfg<D, DEEP>;
+  using C = DecodeCfg<D, DEEP, LIST>;
   return 1024 /*alignment slack*/ + C::kStages * C::kStageBytes + 2 * C::kMiniBytes +
          NT * 8 * D * 2 /*Q*/ + 2 * D * 2 /*new K, V*/ + 2 * C::kStages * 8 /*barriers*/ +
          16 /*flags*/;
@@ -265,11 +268,11 @@ __device__ __forceinline__ void zero_v_chunk(uint8_t *vt, int pstride, int r, in
 // maximum and sum are stored too (DecodeParams::scores), 4 bytes per key and head beside
 // the 4 D of its key and value.
 template <int D, int NT, bool DEEP, int MODE>
-__global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kDecodeList ? 4 : 3)
     decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr bool LIST = MODE == kDecodeList, SCORES = MODE == kDecodeScores;
   constexpr bool LAZY = LIST || SCORES;
-  using Cfg = DecodeCfg<D, DEEP>;
+  using Cfg = DecodeCfg<D, DEEP, LIST>;
   constexpr int kStages = Cfg::kStages;
   constexpr int kHalf = D / 2;
   static_assert(kHalf % 8 == 0, "head dim must be a multiple of 16");
@@ -783,12 +786,12 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 64 ? 3 : 2)
 template <int D, int NT, bool DEEP, int MODE>
 cudaError_t launch_decode_t(const DecodeParams &p, cudaStream_t s, bool pdl) {
   return launch_k(decode_kernel<D, NT, DEEP, MODE>, dim3(p.n_items, p.Hk), dim3(kThreads),
-                  decode_smem_bytes<D, NT, DEEP>(), s, p, pdl);
+                  decode_smem_bytes<D, NT, DEEP, MODE == kDecodeList>(), s, p, pdl);
 }
 
 template <int D, int NT, bool DEEP, int MODE>
 cudaError_t configure_decode_t() {
-  constexpr int smem = decode_smem_bytes<D, NT, DEEP>();
+  constexpr int smem = decode_smem_bytes<D, NT, DEEP, MODE == kDecodeList>();
   return cudaFuncSetAttribute(decode_kernel<D, NT, DEEP, MODE>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }

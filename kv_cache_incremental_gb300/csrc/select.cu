@@ -157,16 +157,17 @@ __device__ __forceinline__ Words<W> load_words(const void *p) {
 // One CTA per (query, kv head).  APPEND (calls of single-token rows): the CTA first rotates
 // and stores its row's new key and value, and computes the bounds of the row's pending
 // blocks, so that a step needs no launches of their own for them.
-// T threads.
+// T threads; the bound keeps a batch of 512 (query, kv head) pairs at D = 128 in one wave.
 template <int D, bool APPEND, int T>
-__global__ void __launch_bounds__(T) select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(T, T == 1024 ? 1 : D == 64 ? 5 : 4)
+    select_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kSelThreads = T, kSelWarps = T / 32;
   static_assert(T >= kCountMax && T >= 256, "a thread per counted candidate and per bin");
   constexpr int kHalf = D / 2;
   extern __shared__ __align__(16) uint8_t sm[];
   int8_t *q8 = reinterpret_cast<int8_t *>(sm);                     // [rep][2][D]: q+, q-
   float *qs = reinterpret_cast<float *>(sm + kMaxRep * 2 * D);     // [rep]
-  uint32_t *keys = reinterpret_cast<uint32_t *>(sm + kSelHead<D>);  // [max_cand]
+  uint32_t *keys = reinterpret_cast<uint32_t *>(sm + kSelHead<D>);  // [max_cand], to a 4
   __shared__ int hist[256];
   __shared__ int warp_n[kSelWarps][2];
   __shared__ int pick[3];  // the digit that holds the threshold, keys above it and in it
@@ -281,9 +282,9 @@ __global__ void __launch_bounds__(T) select_kernel(const __grid_constant__ Selec
     const int8_t *bound = p.bound + ((int64_t)qu.cache_row * p.Hk + g) * p.nb_cap * 2 * D +
                           4 * kWords * sub;
     const float *scale = p.scale + ((int64_t)qu.cache_row * p.Hk + g) * p.nb_cap;
-    // every lane of a warp takes the same number of passes (the shuffles below)
-    for (int c0 = 0; c0 < n_cand; c0 += kSelThreads / 2) {
-      const int cg = c0 + 4 * (tid / 8);
+    // a warp takes 16 blocks per pass, all of its lanes as many passes (the shuffles below)
+    for (int c0 = 16 * warp; c0 < n_cand; c0 += kSelThreads / 2) {
+      const int cg = c0 + 4 * (lane / 8);
       Words<kWords> hi[4], lo[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(T) select_kernel(const __grid_constant__ Selec
         d += __shfl_xor_sync(0xffffffffu, d, 1);
         best = max(best, order_key(__fmul_rn((float)d, __fmul_rn(qs[h], st))));
       }
-      if ((sub & 1) == 0 && c < n_cand) keys[c] = best;
+      if ((sub & 1) == 0 && c < (n_cand + 3) / 4 * 4) keys[c] = c < n_cand ? best : 0;
     }
   }
   __syncthreads();
@@ -324,12 +325,33 @@ __global__ void __launch_bounds__(T) select_kernel(const __grid_constant__ Selec
   uint32_t prefix = 0;  // keys above it are taken, and the first `ties` at it
   int ties = 0;
   if (n_cand <= kCountMax) {
-    // Each thread ranks one candidate; the taken ones are written in order.
+    // Each thread ranks one candidate: equal keys count if they come before it, which only
+    // within a warp differs from thread to thread.  (Keys past the last are 0: they count
+    // for nobody.)  The taken ones are written in order.
     const uint32_t mine = tid < n_cand ? keys[tid] : 0;
     int rank = 0;
-    for (int j = 0; j < n_cand; ++j) {
-      const uint32_t x = keys[j];
-      rank += x > mine || (x == mine && j < tid);
+    if (32 * warp < n_cand) {
+      const uint4 *keys4 = reinterpret_cast<const uint4 *>(keys);
+      const int n4 = (n_cand + 3) / 4, own = 8 * warp, end = min(own + 8, n4);
+#pragma unroll 4
+      for (int j = 0; j < own; ++j) {
+        const uint4 x = keys4[j];
+        rank += (x.x >= mine) + (x.y >= mine) + (x.z >= mine) + (x.w >= mine);
+      }
+#pragma unroll 4
+      for (int j = own; j < end; ++j) {
+        const uint4 x = keys4[j];
+        const int before = tid - 4 * j;  // keys 4 j .. 4 j + before - 1 come before this one
+        rank += (x.x > mine || (x.x == mine && before > 0)) +
+                (x.y > mine || (x.y == mine && before > 1)) +
+                (x.z > mine || (x.z == mine && before > 2)) +
+                (x.w > mine || (x.w == mine && before > 3));
+      }
+#pragma unroll 4
+      for (int j = end; j < n4; ++j) {
+        const uint4 x = keys4[j];
+        rank += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
+      }
     }
     const bool take = tid < n_cand && rank < p.top_k;
     const uint32_t bt = __ballot_sync(0xffffffffu, take);
@@ -417,7 +439,7 @@ __global__ void __launch_bounds__(T) select_kernel(const __grid_constant__ Selec
 template <int D, bool APPEND, int T>
 cudaError_t launch_select_t(const SelectParams &p, cudaStream_t s, bool pdl) {
   return launch_k(select_kernel<D, APPEND, T>, dim3(p.n_queries, p.Hk), dim3(T),
-                  kSelHead<D> + 4 * (size_t)p.max_cand, s, p, pdl);
+                  kSelHead<D> + 16 * (((size_t)p.max_cand + 3) / 4), s, p, pdl);
 }
 
 // Keys of the longest row (max_len = 2^20: 16384 blocks) take 64 KB of shared memory.
