@@ -2555,6 +2555,7 @@ int accumulate_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
   p.q_row_stride = (int64_t)C * Hq * D;
   p.rope = c->rope;
   p.part_ml = c->ppart_ml;
+  p.rotated = (__nv_bfloat16 *)c->ppart_o;
   p.acc_out = acc_out;
   p.acc_stride = c->max_len;
   p.Hq = Hq;
@@ -2589,33 +2590,37 @@ int accumulate_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
         // as many rows as the partials hold at one split each
         size_t r1 = r0;
         int64_t vecs = 0, work = 0;
+        const auto eights = [&](const WeightsRow &r) { return ((r.t1 - r.t0) * rep + 7) / 8; };
         while (r1 < rows.size() && r1 - r0 < (size_t)kMaxRowsPerLaunch) {
           const int64_t v = (int64_t)(rows[r1].t1 - rows[r1].t0) * Hq;
           if (vecs + v > cap) break;
           vecs += v;
-          work += tiles(rows[r1].slots + rows[r1].t1);
+          work += (int64_t)tiles(rows[r1].slots + rows[r1].n) * eights(rows[r1]);
           ++r1;
         }
-        // pass 1: about two CTAs per SM in all, splits of at least four tiles, longer until
-        // the partials fit
-        int64_t per = std::max<int64_t>(4, (work * Hk + 2 * c->num_sms - 1) / (2 * c->num_sms));
-        for (;; per *= 2) {
+        // A CTA's work is its key tiles times the query vectors (in eights).  Two CTAs are
+        // resident per SM: splits of about an equal share of them, at least four tiles, and
+        // longer ones while the launch would need a second wave or the partials do not fit.
+        const int64_t slots2 = 2LL * c->num_sms;
+        for (int64_t share = (work * Hk + slots2 - 1) / slots2;; share += (share + 7) / 8) {
           int64_t part = 0;
-          int item = 0, longest = 1;
+          int item = 0;
+          bool more = false;  // a row is still split
           for (size_t j = r0; j < r1; ++j) {
             WeightsRow &r = p.rows[j - r0];
             r = rows[j];
             const int nt = tiles(r.slots + r.t1);
-            longest = std::max(longest, nt);
+            const int64_t per = std::max<int64_t>(4, (share + eights(r) - 1) / eights(r));
             r.split_tiles = (int)std::min<int64_t>(per, nt);
             r.n_splits = (nt + r.split_tiles - 1) / r.split_tiles;
+            more |= r.n_splits > 1;
             r.item0 = item;
             r.part = (int32_t)part;
             item += r.n_splits;
             part += (int64_t)r.n_splits * (r.t1 - r.t0) * Hq;
           }
           p.n_items = item;
-          if (part <= cap || per >= longest) break;
+          if (!more || (part <= cap && (int64_t)item * Hk <= slots2)) break;
         }
         p.n_rows = (int)(r1 - r0);
         double kb = 0, fl = 0;

@@ -389,6 +389,7 @@ struct WeightsParams {
   int64_t q_row_stride;
   const float2 *rope;
   float2 *part_ml;         // [part + (split * Hk + g) * n_vec + vec]: max (log2 units), sum
+  __nv_bfloat16 *rotated;  // [part + g * n_vec + vec][D]: the rotated query vectors
   const float *acc_in;     // [B][Hk][acc_stride]
   float *acc_out;
   int acc_stride;

@@ -219,6 +219,12 @@ __global__ void __launch_bounds__(kWThreads, 2)
     __syncthreads();
     load_queries<D, QT>(p, row, g, v0, n_vec, qs, limit);
     __syncthreads();
+    if (split == 0) {  // pass 2 takes the rotated vectors as they are
+      uint4 *dst = reinterpret_cast<uint4 *>(p.rotated + (row.part + (int64_t)g * n_vec + v0) * D);
+      for (int u = threadIdx.x; u < min(8 * QT, n_vec - v0) * (D / 8); u += kWThreads)
+        dst[u] = *reinterpret_cast<const uint4 *>(qs + u / (D / 8) * kQStride<D> +
+                                                  16 * (u % (D / 8)));
+    }
     float nm[QT][2], l[QT][2];  // -m, l
 #pragma unroll
     for (int nt = 0; nt < QT; ++nt) {
@@ -264,8 +270,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
   }
 }
 
-// Pass 2: one CTA per (row, kSumTiles tiles of 128 keys, kv head).  One step as in pass 1;
-// ml holds -m and the reciprocal of the sum.
+// Pass 2: one CTA per (row, kSumTiles tiles of 128 keys, kv head).  One step as in pass 1; ml holds -m and the reciprocal of the sum.
 template <int D, int QT, bool FULL>
 __device__ __forceinline__ void sum_step(const uint4 (&f)[D / 16], const uint8_t *qs,
                                          const int *limit, const float2 *ml,
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, qq = lane & 3;
   const int n_vec = (row.t1 - row.t0) * p.rep;
   const int keys = row.slots + row.n;  // slots whose accumulator the call defines
-  const int kb0 = (blockIdx.x - row.item0) * kSumTiles * kWeightTile + 16 * warp;
+  const int kb0 = ((int)blockIdx.x - row.item0) * kSumTiles * kWeightTile + 16 * warp;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   float sum[kSumTiles][2];
@@ -319,7 +324,13 @@ __global__ void __launch_bounds__(kWThreads, 2)
     uint4 a[D / 32], b[D / 32];
     load_keys<D>(p, row, g, kb0, keys - 1, lane, a, b);
     __syncthreads();
-    load_queries<D, QT>(p, row, g, v0, n_vec, qs, limit);
+    const uint4 *src = reinterpret_cast<const uint4 *>(
+        p.rotated + (row.part + (int64_t)g * n_vec + v0) * D);
+    for (int u = threadIdx.x; u < 8 * QT * (D / 8); u += kWThreads) {
+      const int i = u / (D / 8);
+      *reinterpret_cast<uint4 *>(qs + i * kQStride<D> + 16 * (u % (D / 8))) =
+          v0 + i < n_vec ? src[u] : make_uint4(0, 0, 0, 0);
+    }
     for (int i = threadIdx.x; i < 8 * QT; i += kWThreads) {
       float mm = kNoRef, ll = 0.f;
       if (v0 + i < n_vec) {
@@ -333,6 +344,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
       }
       // a vector past the last: weights 2^(0 - inf) * 0
       ml[i] = v0 + i < n_vec ? make_float2(-mm, 1.f / ll) : make_float2(-INFINITY, 0.f);
+      limit[i] = v0 + i < n_vec ? row.slots + row.t0 + (v0 + i) / p.rep : -1;
     }
     __syncthreads();
 #pragma unroll
