@@ -534,7 +534,8 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
  *   acc_in: host array [n_layers] of device float [src B][Hk][src max_len], set for the
  *     global layers (entries of others are ignored).
  *   acc_out: NULL, or such an array for `dst` ([dst B][Hk][dst max_len]) with NULL where
- *     not wanted: the kept keys' accumulators, moved with them.  acc_out[l] may be acc_in[l]
+ *     not wanted: the kept keys' accumulators, moved with them (a zero's sign and a NaN's
+ *     payload may change).  acc_out[l] may be acc_in[l]
  *     when dst == src; else the two must not overlap.
  *   kept: host array [n_layers] of device int32 [n][Hk][keep], set for the global layers:
  *     receives the source slots of destination slots 0.., -1 past the last.

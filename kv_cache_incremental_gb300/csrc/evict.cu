@@ -28,10 +28,16 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 // HELD: the row's weights stay in shared memory (every launch whose rows fit).
+// The number order_key makes, back to its weight (a NaN to the plain one, -0 to +0).
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  if (k == 0) return __int_as_float(0x7FC00000);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
 template <bool HELD>
 __global__ void __launch_bounds__(kThreads)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ float held[];
+  extern __shared__ uint32_t held[];  // order keys
   __shared__ int hist[kBins];
   __shared__ int warp_n[kWarps][2];
   __shared__ int pick[3];  // the digit that holds the threshold, keys above it and in it
@@ -59,12 +65,13 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int i = i0 + j * kThreads + tid;
-        if (i < it.slots) held[i] = x[j];
-        if (cut && i < n) atomicAdd(&hist[order_key(x[j]) >> 21], 1);
+        const uint32_t k = order_key(x[j]);
+        if (i < it.slots) held[i] = k;
+        if (cut && i < n) atomicAdd(&hist[k >> 21], 1);
       }
     }
   }
-  const auto key_at = [&](int i) { return order_key(HELD ? held[i] : acc[i]); };
+  const auto key_at = [&](int i) { return HELD ? held[i] : order_key(acc[i]); };
   uint32_t prefix = 0;  // keys above it are kept, and the first `ties` at it
   int ties = n;         // a row that keeps everything: every key is at or above 0
   if (cut && want > 0) {
@@ -78,6 +85,7 @@ __global__ void __launch_bounds__(kThreads)
         __syncthreads();
       }
       if (!HELD || pass > 0)
+#pragma unroll 4
         for (int i = tid; i < n; i += kThreads) {
           const uint32_t k = key_at(i);
           if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1);
@@ -125,49 +133,56 @@ __global__ void __launch_bounds__(kThreads)
     // before it.
     const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int a = min(warp * per, n), b = min(a + per, n);
+    const auto keep_slot = [&](int at, int i, uint32_t k) {
+      kept[at] = i;
+      if (HELD && out) out[at] = key_weight(k);
+    };
+    const uint32_t below = (1u << lane) - 1;
     int gt = 0, eq = 0;
+#pragma unroll 4
     for (int i = a + lane; i < b; i += 32) {
       const uint32_t k = key_at(i);
       gt += k > prefix;
-      eq += k == prefix;
+      if (ties > 0) eq += k == prefix;
     }
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      gt += __shfl_xor_sync(0xffffffffu, gt, off);
-      eq += __shfl_xor_sync(0xffffffffu, eq, off);
-    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     __syncthreads();  // warp_n of the last digit has been read
     if (lane == 0) {
       warp_n[warp][0] = gt;
       warp_n[warp][1] = eq;
     }
     __syncthreads();
-    gt = eq = 0;
-    for (int w = 0; w < warp; ++w) {
-      gt += warp_n[w][0];
-      eq += warp_n[w][1];
-    }
-    const uint32_t below = (1u << lane) - 1;
-    for (int i0 = a; i0 < b; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t k = i < b ? key_at(i) : 0;
-      const bool is_gt = i < b && k > prefix, is_eq = i < b && k == prefix;
-      const uint32_t bg = __ballot_sync(0xffffffffu, is_gt);
-      const uint32_t be = __ballot_sync(0xffffffffu, is_eq);
-      const int ng = gt + __popc(bg & below), ne = eq + __popc(be & below);
-      if (is_gt || (is_eq && ne < ties)) {
-        const int at = ng + min(ne, ties);
-        kept[at] = i;
-        if (HELD && out) out[at] = held[i];
+    gt = __reduce_add_sync(0xffffffffu, lane < warp ? warp_n[lane][0] : 0);
+    eq = __reduce_add_sync(0xffffffffu, lane < warp ? warp_n[lane][1] : 0);
+    if (ties == 0) {
+#pragma unroll 4
+      for (int i0 = a; i0 < b; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < b ? key_at(i) : 0;
+        const bool is_gt = i < b && k > prefix;
+        const uint32_t bg = __ballot_sync(0xffffffffu, is_gt);
+        if (is_gt) keep_slot(gt + __popc(bg & below), i, k);
+        gt += __popc(bg);
       }
-      gt += __popc(bg);
-      eq += __popc(be);
+    } else {
+      for (int i0 = a; i0 < b; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < b ? key_at(i) : 0;
+        const bool is_gt = i < b && k > prefix, is_eq = i < b && k == prefix;
+        const uint32_t bg = __ballot_sync(0xffffffffu, is_gt);
+        const uint32_t be = __ballot_sync(0xffffffffu, is_eq);
+        const int ng = gt + __popc(bg & below), ne = eq + __popc(be & below);
+        if (is_gt || (is_eq && ne < ties)) keep_slot(ng + min(ne, ties), i, k);
+        gt += __popc(bg);
+        eq += __popc(be);
+      }
     }
   }
   if (cut) {
     for (int i = tid; i < p.recent; i += kThreads) {
       kept[want + i] = n + i;
-      if (HELD && out) out[want + i] = held[n + i];
+      if (HELD && out) out[want + i] = key_weight(held[n + i]);
     }
   } else {
     for (int i = it.slots + tid; i < p.keep; i += kThreads) kept[i] = -1;
