@@ -64,9 +64,12 @@ class _I32Memo:
 
 
 def _stream_ptr(stream, device):
+    """The stream's handle; by default torch's current stream of a device (or its index), asked
+    for without making a Stream object of it."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        index = device if isinstance(device, int) else device.index
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(index))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -461,14 +464,15 @@ class KVCache:
 
     def storage(self, layer: int):
         """Torch views (K, V) of a layer's storage, [B, Hk, rows, D] bf16; rows = max_len + 1
-        (global, and a hybrid layer's group cache) or R + 1 (sliding).  Zero-copy, valid until
-        the cache is closed (a view keeps its memory when the cache itself is dropped), except
-        for a paged cache's global layers: there each row's blocks are gathered from the pool
-        into a new tensor (slots past the row's blocks are zero)."""
+        (global, and a hybrid layer's group cache) or R + 1 (sliding).  Zero-copy, the same two
+        tensors each time, valid until the cache is closed (a view keeps its memory when the
+        cache itself is dropped), except for a paged cache's global layers: there each row's
+        blocks are gathered from the pool into a new tensor (slots past the row's blocks are
+        zero)."""
         import torch
         views = self._views.get(layer)
         if views is not None:
-            return views[0].detach(), views[1].detach()
+            return views
         kp, vp, lp = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_void_p()
         check(_clib.kv_debug_ptrs(self._h, layer, ctypes.byref(kp), ctypes.byref(vp),
                                  ctypes.byref(lp)))
@@ -495,7 +499,7 @@ class KVCache:
         K = self._bf16_view(kp, shape)
         V = self._bf16_view(vp, shape)
         self._views[layer] = (K, V)
-        return K.detach(), V.detach()
+        return K, V
 
     def block_table(self, row: int):
         """Pool blocks of a row in position order (paged caches; [] otherwise)."""
