@@ -79,7 +79,7 @@ enum kv_status {
     KV_ERR_FULL = 2,   /* lens[row] + n_new > max_len for some row ([G] append, [P] update) */
     KV_ERR_DTYPE = 3,  /* tensor dtype is not bfloat16 (raised by language bindings; [P]) */
     KV_ERR_CUDA = 4,   /* a CUDA runtime call failed */
-    KV_ERR_OOM = 5,    /* device memory allocation failed at create */
+    KV_ERR_OOM = 5,    /* device memory allocation failed at create (or host memory ran out) */
     KV_ERR_DEVICE = 6, /* a kernel reported a timed-out wait (see kv_device_error) */
     KV_ERR_SCRATCH = 7, /* request too large for kv_decode_noalloc's fixed scratch */
     KV_ERR_POOL = 8     /* a paged cache has no free block for the new positions */
@@ -489,8 +489,8 @@ int kv_import_row(kv_cache *c, int row, int keep, const void *src, int64_t bytes
  *   KV_ERR_OOM if the memory cannot be had; freed with the cache.  SYNCHRONISES the device.
  * kv_append_sparse: kv_append on a KV_GLOBAL layer (same q, k, v, n_new, rows, out, effects
  *   and errors) with the attention above for every new token.  0 <= sink, 0 <= top_k,
- *   1 <= recent, sink + top_k + recent <= max_select; KV_ERR_ARG otherwise, on a cache that
- *   is not enabled and on other layer kinds.  `selected` (may be NULL): device int32
+ *   1 <= recent, sink + top_k + recent <= max_select, Bs * C < 2^31; KV_ERR_ARG otherwise, on
+ *   a cache that is not enabled and on other layer kinds.  `selected` (may be NULL): device int32
  *   [Bs][C][Hk][sink + top_k + recent], receives each real token's blocks in ascending
  *   order, then -1; entries of padding tokens are not written.  Bounds of blocks filled by
  *   any other call (kv_append, copies, imports, step graphs) are computed by the next

@@ -2370,7 +2370,8 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
   dp.list_recent = recent;
   static const int no_ring[kMaxRowsPerLaunch] = {};
   // the partials are the cache's own: kMaxSplits slots for each of up to min(B, 512) rows
-  plan_decode_splits(c->num_sms, Hk, n, no_ring, dp, std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
+  plan_decode_splits(c->num_sms, Hk, n, no_ring, dp,
+                     std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
   for (int i = 0; i < n; ++i) dp.rows[i].split_tiles2 = qs[i].slot / kSparseBlock;
   dp.deep_pipeline = 0;
   e = timed(c, KV_KERNEL_DECODE, kv_bytes + 4.0 * n * Hq * D, flops, s,
@@ -2382,7 +2383,7 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
 
 extern "C" {
 
-int kv_sparse_enable(kv_cache *c, int max_select) {
+int kv_sparse_enable(kv_cache *c, int max_select) try {
   if (!c || max_select < 1 || max_select > kMaxSelect || c->sparse.max_select) return KV_ERR_ARG;
   bool any = false;
   for (int k : c->kind) any |= k == KV_GLOBAL;
@@ -2419,9 +2420,11 @@ int kv_sparse_enable(kv_cache *c, int max_select) {
   sp.max_select = max_select;
   c->sparse = sp;
   return KV_OK;
+} catch (...) {  // host memory
+  return KV_ERR_OOM;
 }
 
-int kv_sparse_update(kv_cache *c, int layer, const int32_t *rows, int n_rows, void *stream) {
+int kv_sparse_update(kv_cache *c, int layer, const int32_t *rows, int n_rows, void *stream) try {
   if (!c || layer < 0 || layer >= c->n_layers || c->kind[layer] != KV_GLOBAL ||
       !c->sparse.max_select || n_rows < 0 || n_rows > c->B)
     return KV_ERR_ARG;
@@ -2437,11 +2440,13 @@ int kv_sparse_update(kv_cache *c, int layer, const int32_t *rows, int n_rows, vo
   DeviceGuard guard(c->device);
   c->cur_layer = layer;
   return update_bounds(c, layer, rv, slots, slots, (cudaStream_t)stream);
+} catch (...) {  // host memory
+  return KV_ERR_OOM;
 }
 
 int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const void *v, int Hq,
                      int C, const int32_t *n_new, const int32_t *rows, int Bs, int sink,
-                     int top_k, int recent, void *out, int32_t *selected, void *stream) {
+                     int top_k, int recent, void *out, int32_t *selected, void *stream) try {
   if (!c || layer < 0 || layer >= c->n_layers || Hq != c->Hq || C < 1) return KV_ERR_ARG;
   if (c->kind[layer] != KV_GLOBAL || sink < 0 || top_k < 0 || recent < 1 ||
       (int64_t)sink + top_k + recent > c->sparse.max_select)
@@ -2524,6 +2529,8 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
       batch.push_back(sq);
     }
   return flush();
+} catch (...) {  // host memory
+  return KV_ERR_OOM;
 }
 
 }  // extern "C"
@@ -2717,7 +2724,7 @@ extern "C" {
 
 int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, const void *v, int Hq,
                       int C, const int32_t *n_new, const int32_t *rows, int Bs, int last,
-                      const float *acc_in, float *acc_out, void *out, void *stream) {
+                      const float *acc_in, float *acc_out, void *out, void *stream) try {
   if (!c || layer < 0 || layer >= c->n_layers || Hq != c->Hq || C < 1) return KV_ERR_ARG;
   if (c->kind[layer] != KV_GLOBAL || last < 1) return KV_ERR_ARG;
   std::vector<int32_t> cache_rows;
@@ -2763,6 +2770,8 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
                      (__nv_bfloat16 *)out, s);
   if (rc != KV_OK) return rc;
   return accumulate_weights(c, layer, (const __nv_bfloat16 *)q, C, in, acc_in, acc_out, s);
+} catch (...) {  // host memory
+  return KV_ERR_OOM;
 }
 
 }  // extern "C"
@@ -2787,7 +2796,7 @@ int kv_get_slots(const kv_cache *c, int32_t *slots_out) {
 int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
                   const int32_t *src_rows, int n, int keep, int recent,
                   const float *const *acc_in, float *const *acc_out, int32_t *const *kept,
-                  void *stream) {
+                  void *stream) try {
   if (!dst || !src || n < 0 || (n > 0 && (!dst_rows || !src_rows)) || keep < 1 || recent < 0 ||
       recent > keep || !acc_in || !kept)
     return KV_ERR_ARG;
@@ -3009,6 +3018,8 @@ int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
     if (!in_place(i) || slots[i] > keep) trim_bounds(dst, d, 0);
   }
   return KV_OK;
+} catch (...) {  // host memory
+  return KV_ERR_OOM;
 }
 
 const char *kv_strerror(int code) {

@@ -246,14 +246,14 @@ def test_pool_exhaustion_changes_nothing():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("paged", [False, True])
-def test_going_on_with_evicted_rows(paged):
+@pytest.mark.parametrize("D,paged", [(64, False), (64, True), (128, False), (128, True)])
+def test_going_on_with_evicted_rows(D, paged):
     """After an eviction the other calls append at the next slot, rotate at the true position
     and attend to what is kept: dense decode and chunks, the step graph, sparse and counted
     calls, another eviction, reset, import and copies into the row."""
     import torch
     import kv_cache_incremental_gb300 as kvi
-    r = Rows(4, 900, 8, 2, 64, [700, 300, 64, 500], seed=12, paged=paged)
+    r = Rows(4, 900, 8, 2, D, [700, 300, 64, 500], seed=12, paged=paged)
     r.cache.enable_sparse(5)
     test_sparse.step(r, [1, 1, 1, 1], 1, 2, 2)
     evict(r, r, [0, 1, 3], [0, 1, 3], 200, 30)
@@ -277,11 +277,11 @@ def test_going_on_with_evicted_rows(paged):
     check_state(r)
     # ordinary again
     r.cache.reset([0])
-    r.K[0][0] = r.V[0][0] = np.zeros((2, 0, 64), np.uint16)
+    r.K[0][0] = r.V[0][0] = np.zeros((2, 0, D), np.uint16)
     r.lens[0] = 0
     r.cache.copy_rows(r.cache, [2], [1])
     r.K[0][1], r.V[0][1], r.lens[1] = r.K[0][2], r.V[0][2], r.lens[2]
-    r.K[0][3], r.V[0][3], r.lens[3] = r.bits((2, 40, 64)), r.bits((2, 40, 64)), 40
+    r.K[0][3], r.V[0][3], r.lens[3] = r.bits((2, 40, D)), r.bits((2, 40, D)), 40
     r.fill(3, 40)
     dense_step(r, [30, 1, 1, 1])
     test_sparse.step(r, [1, 1, 1, 66], 1, 1, 1)
@@ -434,6 +434,52 @@ def test_generation_within_a_budget():
                     acc[b, :, r.cache.slots[b] - 1] = 0
         check_state(r)
     assert r.cache.device_error() == 0
+
+
+@pytest.mark.gpu
+def test_two_caches_on_two_streams_at_once():
+    """Calls of two caches queued on two streams with nothing waiting between them."""
+    import torch
+    rs = [Rows(3, 900, 8, 2, 64, [800, 300, 500], seed=90 + i, paged=i == 1) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in rs]
+    work = []
+    for r in rs:
+        r.cache.enable_sparse(4)
+        qkv = [[dev(x) for x in r.tokens(3, 1)] for _ in range(3)]
+        acc = torch.rand((3, 2, 900), device="cuda")
+        work.append((qkv, acc))
+    torch.cuda.synchronize()
+    results = [[], []]
+    for turn in range(2):           # in turn, then alone: the same results
+        if turn == 1:
+            rs = [Rows(3, 900, 8, 2, 64, [800, 300, 500], seed=90 + i, paged=i == 1)
+                  for i in range(2)]
+            for r in rs:
+                r.cache.enable_sparse(4)
+            torch.cuda.synchronize()
+        accs_ = [w[1].clone() for w in work]
+        torch.cuda.synchronize()
+        outs = [[], []]
+        for step in range(3):
+            for i, r in enumerate(rs):
+                s, (q, k, v) = streams[i], work[i][0][step]
+                if step == 0:
+                    o = r.cache.append_weights(0, q, k, v, [1] * 3, accs_[i], accs_[i], stream=s)
+                elif step == 1:
+                    r.cache.evict([0, 2], 200, 30, [accs_[i]], stream=s)
+                    o = r.cache.append_sparse(0, q, k, v, [1] * 3, 1, stream=s)
+                else:
+                    o = r.cache.append(0, q, k, v, [1] * 3, stream=s)
+                r.cache.advance([1] * 3, stream=s)
+                outs[i].append(o)
+                if turn == 1:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        for i in range(2):
+            results[turn].append([bits_of(o) for o in outs[i]] + [accs_[i].cpu().numpy()])
+    for a, b in zip(*results):
+        for x, y in zip(a, b):
+            assert np.array_equal(x, y)
 
 
 @pytest.mark.gpu
