@@ -57,12 +57,16 @@ constexpr int kMiniRows = 16;  // rows of the new-key mini-tile
 // twice the bytes in flight to keep HBM busy.  LIST at D = 64: three stages and four CTAs per
 // SM, since chunks read their blocks from L2 and the CTAs' chains of tiles bound them (24 rows
 // with chunks of up to 64 tokens over 19 blocks, the whole call: 101.7 -> 96.3 us; at D = 128
-// two stages and three CTAs lost, 16 rows over 37 blocks 40.4 -> 42.8).
+// two stages and three CTAs lost, 16 rows over 37 blocks 40.4 -> 42.8).  LIST with DEEP: five
+// (six) stages, so that more of the blocks known before the selection stream while it runs (16
+// rows over 37 blocks, 128 CTAs: 41.1 us with three stages, 37.8 with four or five, 38.2 with
+// six; 64 rows over 19 blocks, 512 CTAs, would go from 58.5 to 67).
 template <int D, bool DEEP, bool LIST = false>
 struct DecodeCfg {
   static constexpr int kPanels = D / 64;                        // 128-byte swizzle panels
   static constexpr int kTileBytes = kPanels * kTileKeys * 128;  // one K or V tile
-  static constexpr int kStages = (D == 128 || LIST ? 3 : 4) * (DEEP ? 2 : 1);
+  static constexpr int kStages =
+      LIST && DEEP ? (D == 128 ? 5 : 6) : (D == 128 || LIST ? 3 : 4) * (DEEP ? 2 : 1);
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kMiniBytes = kPanels * kMiniRows * 128;  // one K or V mini-tile
 };

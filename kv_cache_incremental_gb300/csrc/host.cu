@@ -2373,7 +2373,7 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
   plan_decode_splits(c->num_sms, Hk, n, no_ring, dp,
                      std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
   for (int i = 0; i < n; ++i) dp.rows[i].split_tiles2 = qs[i].slot / kSparseBlock;
-  dp.deep_pipeline = 0;
+  if (!c->pdl) dp.deep_pipeline = 0;
   e = timed(c, KV_KERNEL_DECODE, kv_bytes + 4.0 * n * Hq * D, flops, s,
             [&] { return launch_decode(dp, D, dp.rep <= 8 ? 1 : 2, s, c->pdl); });
   return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
