@@ -796,7 +796,7 @@ def run_ours(args, sub=False):
     tok_s = world * B * K / (ms / 1e3)
     dec = prof["decode"]
     achieved = dec["bytes"] / (dec["ms"] / 1e3) / 1e9 if dec["ms"] > 0 else None
-    traffic = traffic_record("decode.cu", args.workload)
+    traffic = traffic_record("decode_kernel.cuh", args.workload)
     roofline = {
         "bound": "hbm", "achieved": achieved, "peak": peak, "unit": "GB/s",
         "frac": (achieved / peak) if achieved else None,

@@ -409,6 +409,14 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
     // ------------------------------------------------------------ producer
     // One copy of the loop per segment, so that each names its tensor maps by their
     // fixed parameter addresses.
+    // SCORES: keys and values pass through L2 once and leave it first, so that the scores stay
+    // there for the join while they fit (38 MB of them, 64 rows of 1k-8k keys, Hq = 32: 197 ->
+    // 190 us; 100 MB, 16 rows of 16k-32k keys, Hq = 64: 294 either way).
+    const uint64_t policy = SCORES ? ptx::policy_evict_first() : 0;
+    auto load = [&](void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar) {
+      if (SCORES) ptx::tma_load_2d_hint(dst, m, x, y, bar, policy);
+      else ptx::tma_load_2d(dst, m, x, y, bar);
+    };
     auto produce = [&](const CUtensorMap *map_k, const CUtensorMap *map_v) {
       ptx::prefetch_tmap(map_k);
       ptx::prefetch_tmap(map_v);
@@ -427,16 +435,16 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
           const int y = static_cast<int>(row0 + (int64_t)it * kTileKeys);
 #pragma unroll
           for (int pn = 0; pn < Cfg::kPanels; ++pn) {
-            ptx::tma_load_2d(kt + pn * kTileKeys * 128, map_k, pn * 64, y, &full[s]);
-            ptx::tma_load_2d(vt + pn * kTileKeys * 128, map_v, pn * 64, y, &full[s]);
+            load(kt + pn * kTileKeys * 128, map_k, pn * 64, y, &full[s]);
+            load(vt + pn * kTileKeys * 128, map_v, pn * 64, y, &full[s]);
           }
         } else {  // paged: the tile's four 16-key blocks, one box when consecutive
           const int4 y4 = kv_rows4(pt, row.cache_row, g, k0 + it * kTileKeys);
           if (rows4_contiguous(y4)) {
 #pragma unroll
             for (int pn = 0; pn < Cfg::kPanels; ++pn) {
-              ptx::tma_load_2d(kt + pn * kTileKeys * 128, &p.tmap_k, pn * 64, y4.x, &full[s]);
-              ptx::tma_load_2d(vt + pn * kTileKeys * 128, &p.tmap_v, pn * 64, y4.x, &full[s]);
+              load(kt + pn * kTileKeys * 128, &p.tmap_k, pn * 64, y4.x, &full[s]);
+              load(vt + pn * kTileKeys * 128, &p.tmap_v, pn * 64, y4.x, &full[s]);
             }
           } else {
             const int ys[4] = {y4.x, y4.y, y4.z, y4.w};
@@ -445,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
 #pragma unroll
               for (int pn = 0; pn < Cfg::kPanels; ++pn) {
                 const int off = pn * kTileKeys * 128 + j * kBlockTokens * 128;
-                ptx::tma_load_2d(kt + off, &p.tmap_k16, pn * 64, ys[j], &full[s]);
-                ptx::tma_load_2d(vt + off, &p.tmap_v16, pn * 64, ys[j], &full[s]);
+                load(kt + off, &p.tmap_k16, pn * 64, ys[j], &full[s]);
+                load(vt + off, &p.tmap_v16, pn * 64, ys[j], &full[s]);
               }
             }
           }
