@@ -110,7 +110,8 @@ struct WarpAcc {
 // SCORES: the visible keys' scores go to scores[h * score_stride + key], h < rep.
 // LAZY: the running maximum moves only when a score exceeds it by kSlack, so that most steps
 // have no exchange between lanes and no rescaling; weights then reach 2^kSlack, which neither
-// their bf16 halves nor the float sums mind.
+// their bf16 halves nor the float sums mind (chunks over listed blocks 108 -> 103 us, counted
+// decode of 64 rows 198.5 -> 195.9).
 constexpr float kSlack = 8.f;
 template <int D, int NT, bool SCORES, bool LAZY>
 __device__ __forceinline__ void attend16(WarpAcc<D, NT> &acc, const uint32_t (&qb)[NT][D / 16][2],

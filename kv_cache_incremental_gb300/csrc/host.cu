@@ -2573,88 +2573,84 @@ int accumulate_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
   p.pt = page_table(c, layer);
   const auto tiles = [](int keys) { return (keys + kWeightTile - 1) / kWeightTile; };
-  // the launches' rows of one kind (see launch_weights): single tokens apart from chunks
-  for (int kind = 0; kind < 2; ++kind) {
-    int most = 0;
-    for (const WeightsIn &w : in)
-      if ((w.n - w.t0 == 1) == (kind == 0)) most = std::max(most, w.n - w.t0);
-    for (int g0 = 0; g0 < most; g0 += group) {
-      std::vector<WeightsRow> rows;
-      for (const WeightsIn &w : in) {
-        if ((w.n - w.t0 == 1) != (kind == 0) || w.n - w.t0 <= g0) continue;
-        WeightsRow r = {};
-        r.cache_row = w.cache_row;
-        r.call_row = w.call_row;
-        r.slots = slots_of(c, w.cache_row);
-        r.shift = c->dropped[w.cache_row];
-        r.n = w.n;
-        r.t0 = w.t0 + g0;
-        r.t1 = std::min(w.n, r.t0 + group);
-        r.first = g0 == 0 ? 1 : 0;
-        rows.push_back(r);
+  int most = 0;
+  for (const WeightsIn &w : in) most = std::max(most, w.n - w.t0);
+  for (int g0 = 0; g0 < most; g0 += group) {
+    std::vector<WeightsRow> rows;
+    for (const WeightsIn &w : in) {
+      if (w.n - w.t0 <= g0) continue;
+      WeightsRow r = {};
+      r.cache_row = w.cache_row;
+      r.call_row = w.call_row;
+      r.slots = slots_of(c, w.cache_row);
+      r.shift = c->dropped[w.cache_row];
+      r.n = w.n;
+      r.t0 = w.t0 + g0;
+      r.t1 = std::min(w.n, r.t0 + group);
+      r.first = g0 == 0 ? 1 : 0;
+      rows.push_back(r);
+    }
+    for (size_t r0 = 0; r0 < rows.size();) {
+      // as many rows as the partials hold at one split each
+      size_t r1 = r0;
+      int64_t vecs = 0, work = 0;
+      const auto eights = [&](const WeightsRow &r) { return ((r.t1 - r.t0) * rep + 7) / 8; };
+      while (r1 < rows.size() && r1 - r0 < (size_t)kMaxRowsPerLaunch) {
+        const int64_t v = (int64_t)(rows[r1].t1 - rows[r1].t0) * Hq;
+        if (vecs + v > cap) break;
+        vecs += v;
+        work += (int64_t)tiles(rows[r1].slots + rows[r1].n) * eights(rows[r1]);
+        ++r1;
       }
-      for (size_t r0 = 0; r0 < rows.size();) {
-        // as many rows as the partials hold at one split each
-        size_t r1 = r0;
-        int64_t vecs = 0, work = 0;
-        const auto eights = [&](const WeightsRow &r) { return ((r.t1 - r.t0) * rep + 7) / 8; };
-        while (r1 < rows.size() && r1 - r0 < (size_t)kMaxRowsPerLaunch) {
-          const int64_t v = (int64_t)(rows[r1].t1 - rows[r1].t0) * Hq;
-          if (vecs + v > cap) break;
-          vecs += v;
-          work += (int64_t)tiles(rows[r1].slots + rows[r1].n) * eights(rows[r1]);
-          ++r1;
-        }
-        // A CTA's work is its key tiles times the query vectors (in eights).  Two CTAs are
-        // resident per SM: splits of about an equal share of them, at least four tiles, and
-        // longer ones while the launch would need a second wave or the partials do not fit.
-        const int64_t slots2 = 2LL * c->num_sms;
-        for (int64_t share = (work * Hk + slots2 - 1) / slots2;; share += (share + 7) / 8) {
-          int64_t part = 0;
-          int item = 0;
-          bool more = false;  // a row is still split
-          for (size_t j = r0; j < r1; ++j) {
-            WeightsRow &r = p.rows[j - r0];
-            r = rows[j];
-            const int nt = tiles(r.slots + r.t1);
-            const int64_t per = std::max<int64_t>(4, (share + eights(r) - 1) / eights(r));
-            r.split_tiles = (int)std::min<int64_t>(per, nt);
-            r.n_splits = (nt + r.split_tiles - 1) / r.split_tiles;
-            more |= r.n_splits > 1;
-            r.item0 = item;
-            r.part = (int32_t)part;
-            item += r.n_splits;
-            part += (int64_t)r.n_splits * (r.t1 - r.t0) * Hq;
-          }
-          p.n_items = item;
-          if (!more || (part <= cap && (int64_t)item * Hk <= slots2)) break;
-        }
-        p.n_rows = (int)(r1 - r0);
-        double kb = 0, fl = 0;
-        for (int j = 0; j < p.n_rows; ++j) {
-          const WeightsRow &r = p.rows[j];
-          kb += 2.0 * (r.slots + r.t1) * Hk * D;
-          fl += 2.0 * (r.slots + r.t1) * (double)(r.t1 - r.t0) * Hq * D;
-        }
-        p.acc_in = g0 == 0 ? acc_in : acc_out;
-        cudaError_t e = timed(c, KV_KERNEL_WEIGHTS, kb, fl, s,
-                              [&] { return launch_weights(p, 1, s, c->pdl); });
-        if (e != cudaSuccess) return KV_ERR_CUDA;
-        // pass 2: CTAs over every slot that the call defines
+      // A CTA's work is its key tiles times the query vectors (in eights).  Two CTAs are
+      // resident per SM: splits of about an equal share of them, at least four tiles, and
+      // longer ones while the launch would need a second wave or the partials do not fit.
+      const int64_t slots2 = 2LL * c->num_sms;
+      for (int64_t share = (work * Hk + slots2 - 1) / slots2;; share += (share + 7) / 8) {
+        int64_t part = 0;
         int item = 0;
-        double ab = 0;
-        for (int j = 0; j < p.n_rows; ++j) {
-          WeightsRow &r = p.rows[j];
+        bool more = false;  // a row is still split
+        for (size_t j = r0; j < r1; ++j) {
+          WeightsRow &r = p.rows[j - r0];
+          r = rows[j];
+          const int nt = tiles(r.slots + r.t1);
+          const int64_t per = std::max<int64_t>(4, (share + eights(r) - 1) / eights(r));
+          r.split_tiles = (int)std::min<int64_t>(per, nt);
+          r.n_splits = (nt + r.split_tiles - 1) / r.split_tiles;
+          more |= r.n_splits > 1;
           r.item0 = item;
-          item += (tiles(r.slots + r.n) + kWeightSumTiles - 1) / kWeightSumTiles;
-          ab += 8.0 * (r.slots + r.n) * Hk;
+          r.part = (int32_t)part;
+          item += r.n_splits;
+          part += (int64_t)r.n_splits * (r.t1 - r.t0) * Hq;
         }
         p.n_items = item;
-        e = timed(c, KV_KERNEL_WEIGHTS, kb + ab, fl, s,
-                  [&] { return launch_weights(p, 2, s, c->pdl); });
-        if (e != cudaSuccess) return KV_ERR_CUDA;
-        r0 = r1;
+        if (!more || (part <= cap && (int64_t)item * Hk <= slots2)) break;
       }
+      p.n_rows = (int)(r1 - r0);
+      double kb = 0, fl = 0;
+      for (int j = 0; j < p.n_rows; ++j) {
+        const WeightsRow &r = p.rows[j];
+        kb += 2.0 * (r.slots + r.t1) * Hk * D;
+        fl += 2.0 * (r.slots + r.t1) * (double)(r.t1 - r.t0) * Hq * D;
+      }
+      p.acc_in = g0 == 0 ? acc_in : acc_out;
+      cudaError_t e = timed(c, KV_KERNEL_WEIGHTS, kb, fl, s,
+                            [&] { return launch_weights(p, 1, s, c->pdl); });
+      if (e != cudaSuccess) return KV_ERR_CUDA;
+      // pass 2: CTAs over every slot that the call defines
+      int item = 0;
+      double ab = 0;
+      for (int j = 0; j < p.n_rows; ++j) {
+        WeightsRow &r = p.rows[j];
+        r.item0 = item;
+        item += (tiles(r.slots + r.n) + kWeightSumTiles - 1) / kWeightSumTiles;
+        ab += 8.0 * (r.slots + r.n) * Hk;
+      }
+      p.n_items = item;
+      e = timed(c, KV_KERNEL_WEIGHTS, kb + ab, fl, s,
+                [&] { return launch_weights(p, 2, s, c->pdl); });
+      if (e != cudaSuccess) return KV_ERR_CUDA;
+      r0 = r1;
     }
   }
   return KV_OK;

@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kBoundsWarps * 32)
 
 // ---------------------------------------------------------------- selection
 // Up to this many candidates a block's rank is counted directly (every candidate against
-// every other), above it found by radix selection.
+// every other), above it found by radix selection (16 to 125 candidates, 64 rows, the whole
+// call: counted 58.0 us, by radix 59.1; 29 candidates, one row: 9.9 and 11.1).
 constexpr int kCountMax = 256;
 
 // Order-preserving whole number of a score: NaN lowest, -0 and +0 alike.

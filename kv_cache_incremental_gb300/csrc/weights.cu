@@ -7,8 +7,9 @@
 // A weight needs its query's m and l over all keys first.  For rows with a single new token
 // the decode kernel stores the scores on its one pass over K and V (decode_kernel.cuh, the
 // scores mode) and the join kernel turns them into weights: 8 bytes of scores per key and
-// head, written and read, beside the 4 D bytes of a key and value.  For chunks, and for rows
-// whose scores outgrow the room reserved for them, there are two passes over K: the first leaves (m, l) per query vector and key split, the second joins the splits and
+// head, written and read, beside the 4 D bytes of a key and value (64 rows of 1k-8k keys, Hq
+// 32, Hk 8, D 128: 190 us, 489 with two passes).  For chunks, and for rows whose scores
+// outgrow the room reserved for them, there are two passes over K: the first leaves (m, l) per query vector and key split, the second joins the splits and
 // sums the weights per key.  Both form S^T = K Q^T with mma.sync (keys on M, query vectors
 // on N): a key's weights then lie in the lanes of one quad and its sum over the queries
 // stays in a register; a query's running (m, l) over its lane's keys stays in registers
@@ -27,6 +28,10 @@ namespace {
 
 constexpr int kWarps = 8, kWThreads = kWarps * 32;
 constexpr int kSumTiles = kWeightSumTiles;
+// Query vectors are taken in chunks of 8 QT.  A chunk's unused eights are skipped: variants of
+// one and two eights for single tokens ran no faster (8 counted vectors, 24 rows of 6k keys:
+// 54.7 us with eight, 54.9 with one).
+constexpr int QT = 8;
 static_assert(kWeightTile == kWarps * 16, "one 16-key fragment per warp");
 
 __device__ __forceinline__ int find_weights_row(const WeightsParams &p, int item) {
@@ -47,7 +52,7 @@ constexpr int kQStride = 2 * D + 64;
 // Query vectors [v0, v0 + 8 QT) of the row, rotated and rounded to bf16 as the attention
 // rotates them, into shared memory, and the last slot that each sees; vectors past the last
 // are zero and see nothing.
-template <int D, int QT>
+template <int D>
 __device__ __forceinline__ void load_queries(const WeightsParams &p, const WeightsRow &row, int g,
                                              int v0, int n_vec, uint8_t *qs, int *limit) {
   constexpr int kHalf = D / 2, kVec = kHalf / 8;
@@ -154,15 +159,15 @@ constexpr float kNoRef = -1e30f, kSlack = 64.f;
 //
 // One step: 16 keys as fragments f against the first n_nt eights of query vectors.  FULL: every key
 // is visible to every vector; else key gq is visible up to `limit` and below k1.
-template <int D, int QT, bool FULL>
+template <int D, bool FULL>
 __device__ __forceinline__ void stats_step(const uint4 (&f)[D / 16], const uint8_t *qs,
                                            const int *limit, int n_nt, int key, int k1,
                                            float scale, int lane, float (&nm)[QT][2],
                                            float (&l)[QT][2]) {
-  constexpr int N = QT > 1 ? 2 : 1;
+  constexpr int N = 2;
 #pragma unroll
   for (int nt0 = 0; nt0 < QT; nt0 += N) {
-    if (QT > 1 && nt0 >= n_nt) break;
+    if (nt0 >= n_nt) break;
     float sc[N][4];
     scores<D, N>(f, qs, nt0, lane, sc);
 #pragma unroll
@@ -197,7 +202,7 @@ __device__ __forceinline__ void stats_step(const uint4 (&f)[D / 16], const uint8
   }
 }
 
-template <int D, int QT>
+template <int D>
 __global__ void __launch_bounds__(kWThreads, 2)
     weights_stats_kernel(const __grid_constant__ WeightsParams p) {
   __shared__ __align__(16) uint8_t qs[8 * QT * kQStride<D>];
@@ -217,7 +222,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
     uint4 a[D / 32], b[D / 32];
     if (k0 + 16 * warp < k1) load_keys<D>(p, row, g, k0 + 16 * warp, keys - 1, lane, a, b);
     __syncthreads();
-    load_queries<D, QT>(p, row, g, v0, n_vec, qs, limit);
+    load_queries<D>(p, row, g, v0, n_vec, qs, limit);
     __syncthreads();
     if (split == 0) {  // pass 2 takes the rotated vectors as they are
       uint4 *dst = reinterpret_cast<uint4 *>(p.rotated + (row.part + (int64_t)g * n_vec + v0) * D);
@@ -237,13 +242,13 @@ __global__ void __launch_bounds__(kWThreads, 2)
       if (kb + kWeightTile < k1)  // the next keys, while these are used
         load_keys<D>(p, row, g, kb + kWeightTile, keys - 1, lane, a, b);
       if (kb + 16 <= k1 && kb + 15 <= row.slots + row.t0)
-        stats_step<D, QT, true>(f, qs, limit, n_nt, kb + gq, k1, p.scale_log2, lane, nm, l);
+        stats_step<D, true>(f, qs, limit, n_nt, kb + gq, k1, p.scale_log2, lane, nm, l);
       else
-        stats_step<D, QT, false>(f, qs, limit, n_nt, kb + gq, k1, p.scale_log2, lane, nm, l);
+        stats_step<D, false>(f, qs, limit, n_nt, kb + gq, k1, p.scale_log2, lane, nm, l);
     }
 #pragma unroll
     for (int nt = 0; nt < QT; ++nt) {
-      if (QT > 1 && nt >= n_nt) break;
+      if (nt >= n_nt) break;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float m = -nm[nt][j];
@@ -271,15 +276,15 @@ __global__ void __launch_bounds__(kWThreads, 2)
 }
 
 // Pass 2: one CTA per (row, kSumTiles tiles of 128 keys, kv head).  One step as in pass 1; ml holds -m and the reciprocal of the sum.
-template <int D, int QT, bool FULL>
+template <int D, bool FULL>
 __device__ __forceinline__ void sum_step(const uint4 (&f)[D / 16], const uint8_t *qs,
                                          const int *limit, const float2 *ml,
                                          int n_nt, int key, float scale, int lane, float &sum0,
                                          float &sum1) {
-  constexpr int N = QT > 1 ? 2 : 1;
+  constexpr int N = 2;
 #pragma unroll
   for (int nt0 = 0; nt0 < QT; nt0 += N) {
-    if (QT > 1 && nt0 >= n_nt) break;
+    if (nt0 >= n_nt) break;
     float sc[N][4];
     scores<D, N>(f, qs, nt0, lane, sc);
 #pragma unroll
@@ -302,7 +307,7 @@ __device__ __forceinline__ void sum_step(const uint4 (&f)[D / 16], const uint8_t
   }
 }
 
-template <int D, int QT>
+template <int D>
 __global__ void __launch_bounds__(kWThreads, 2)
     weights_sum_kernel(const __grid_constant__ WeightsParams p) {
   __shared__ __align__(16) uint8_t qs[8 * QT * kQStride<D>];
@@ -356,10 +361,10 @@ __global__ void __launch_bounds__(kWThreads, 2)
       if (i + 1 < kSumTiles && kb + kWeightTile < keys)
         load_keys<D>(p, row, g, kb + kWeightTile, keys - 1, lane, a, b);
       if (kb + 15 <= row.slots + row.t0)
-        sum_step<D, QT, true>(f, qs, limit, ml, n_nt, kb + gq, p.scale_log2, lane, sum[i][0],
+        sum_step<D, true>(f, qs, limit, ml, n_nt, kb + gq, p.scale_log2, lane, sum[i][0],
                               sum[i][1]);
       else
-        sum_step<D, QT, false>(f, qs, limit, ml, n_nt, kb + gq, p.scale_log2, lane, sum[i][0],
+        sum_step<D, false>(f, qs, limit, ml, n_nt, kb + gq, p.scale_log2, lane, sum[i][0],
                                sum[i][1]);
     }
   }
@@ -419,13 +424,6 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
     if (s0 + 256 * i < row.keys) p.acc_out[at + 256 * i] = sum[i];
 }
 
-template <int D, int QT>
-cudaError_t launch_weights_t(const WeightsParams &p, int pass, cudaStream_t s, bool pdl) {
-  const dim3 grid(p.n_items, p.Hk), block(kWThreads);
-  return pass == 1 ? launch_k(weights_stats_kernel<D, QT>, grid, block, 0, s, p, pdl)
-                   : launch_k(weights_sum_kernel<D, QT>, grid, block, 0, s, p, pdl);
-}
-
 }  // namespace
 
 cudaError_t launch_join(const JoinParams &p, cudaStream_t s, bool pdl) {
@@ -433,22 +431,14 @@ cudaError_t launch_join(const JoinParams &p, cudaStream_t s, bool pdl) {
   return launch_k(join_kernel, dim3(p.n_items, p.Hk), dim3(256), 0, s, p, pdl);
 }
 
-// Rows of a launch are of one kind: at most 8 query vectors (single tokens of groups of up
-// to 8 heads) in one fragment, at most 16 in two, else chunks of 64.
 cudaError_t launch_weights(const WeightsParams &p, int pass, cudaStream_t s, bool pdl) {
   if (p.n_items <= 0) return cudaSuccess;
-  int most = 0;
-  for (int i = 0; i < p.n_rows; ++i)
-    most = p.rows[i].t1 - p.rows[i].t0 > most ? p.rows[i].t1 - p.rows[i].t0 : most;
-  most *= p.rep;
-  if (p.D == 128) {
-    if (most <= 8) return launch_weights_t<128, 1>(p, pass, s, pdl);
-    if (most <= 16) return launch_weights_t<128, 2>(p, pass, s, pdl);
-    return launch_weights_t<128, 8>(p, pass, s, pdl);
-  }
-  if (most <= 8) return launch_weights_t<64, 1>(p, pass, s, pdl);
-  if (most <= 16) return launch_weights_t<64, 2>(p, pass, s, pdl);
-  return launch_weights_t<64, 8>(p, pass, s, pdl);
+  const dim3 grid(p.n_items, p.Hk), block(kWThreads);
+  if (p.D == 128)
+    return pass == 1 ? launch_k(weights_stats_kernel<128>, grid, block, 0, s, p, pdl)
+                     : launch_k(weights_sum_kernel<128>, grid, block, 0, s, p, pdl);
+  return pass == 1 ? launch_k(weights_stats_kernel<64>, grid, block, 0, s, p, pdl)
+                   : launch_k(weights_sum_kernel<64>, grid, block, 0, s, p, pdl);
 }
 
 }  // namespace kvinc
