@@ -40,7 +40,7 @@ bool pick(int D, int n_tiles_heads, bool deep, void **fn, int *smem) {
 cudaError_t launch_decode(const DecodeParams &p, int D, int n_tiles_heads, cudaStream_t s,
                           bool pdl) {
   if (p.list) return launch_decode_list(p, D, n_tiles_heads, s, pdl);
-  if (p.scores) return launch_decode_scores(p, D, n_tiles_heads, s, pdl);
+  if (p.row_ml) return launch_decode_scores(p, D, n_tiles_heads, s, pdl);
   return launch_decode_mode<kDecodePlain>(p, D, n_tiles_heads, s, pdl);
 }
 

@@ -145,7 +145,7 @@ __device__ __forceinline__ void attend16(WarpAcc<D, NT> &acc, const uint32_t (&q
     const float t1 = va ? sacc[nt][1] * scale_log2 : -INFINITY;
     const float t2 = vb ? sacc[nt][2] * scale_log2 : -INFINITY;
     const float t3 = vb ? sacc[nt][3] * scale_log2 : -INFINITY;
-    if (SCORES) {
+    if (SCORES && scores) {
       const int h = nt * 8 + 2 * (lane & 3);
       float *s0 = scores + h * score_stride + gq, *s1 = s0 + score_stride;
       if (h < rep) {
@@ -269,9 +269,9 @@ __device__ __forceinline__ void zero_v_chunk(uint8_t *vt, int pstride, int r, in
 // spilled at D = 64).
 // MODE kDecodeList: the row's tiles are the blocks of a list (sparse attention,
 // DecodeParams::list); the launch appends nothing, so a tile's masked keys are only the slots
-// past the last block's end.  kDecodeScores: every key's scores and each head's softmax
-// maximum and sum are stored too (DecodeParams::scores), 4 bytes per key and head beside
-// the 4 D of its key and value.
+// past the last block's end.  kDecodeScores: each head's softmax maximum and sum are stored
+// too (DecodeParams::row_ml) and, if wanted, every key's scores, 4 bytes per key and head
+// beside the 4 D of its key and value.
 template <int D, int NT, bool DEEP, int MODE>
 __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kDecodeList ? 4 : 3)
     decode_kernel(const __grid_constant__ DecodeParams p) {
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
   }
 
   float *scores = nullptr;  // of the row's query heads of this kv head
-  if (SCORES)
+  if (SCORES && p.scores)
     scores = p.scores + ((int64_t)row_idx * p.Hq + g * p.rep) * p.score_stride;
   for (int it = 0; it < n_tiles; ++it) {
     const int s = it % kStages;
@@ -622,14 +622,14 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
       __syncwarp();
     }
     attend16<D, NT, SCORES, LAZY>(acc, qb, kt, vt, kTileKeys * 128, 16 * warp, n_valid,
-                            skip_here ? skip : -1, p.scale_log2, lane, scores + key_base,
+                            skip_here ? skip : -1, p.scale_log2, lane, scores ? scores + key_base : nullptr,
                             p.score_stride, p.rep);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&empty[s]);
   }
   if (owner && warp == 0 && !*fail)  // the new key, from the mini-tile (row 0 only)
     attend16<D, NT, SCORES, LAZY>(acc, qb, mini_k, mini_v, kMiniRows * 128, 0, 1, -1, p.scale_log2, lane,
-                            scores + new_slot, p.score_stride, p.rep);
+                            scores ? scores + new_slot : nullptr, p.score_stride, p.rep);
 
   // ---------------------------------------------------------------- merge warps
   // All consumers are past their last tile before the stage memory is reused.
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
     for (int w = 0; w < kConsumerWarps; ++w) wsm[w * kH + h] = f[w] * sc;
     if (!single) p.part_ml[part * p.Hq + g * p.rep + h] = make_float2(m, l);
     if (SCORES && single)
-      p.row_ml[(int64_t)row_idx * p.Hq + g * p.rep + h] = make_float2(m, 1.f / l);
+      p.row_ml[(int64_t)row.call_row * kChunk * p.Hq + g * p.rep + h] = make_float2(m, 1.f / l);
   }
   consumer_sync();
   for (int u = threadIdx.x; u < p.rep * (D / 8); u += kConsumerWarps * 32) {
@@ -772,7 +772,8 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
     float l = 0.f;
     for (int sp = 0; sp < ns; ++sp) l += exp2f(wml[sp * p.rep + h].x - m) * wml[sp * p.rep + h].y;
     const float inv = 1.f / l;
-    if (SCORES) p.row_ml[(int64_t)row_idx * p.Hq + g * p.rep + h] = make_float2(m, inv);
+    if (SCORES)
+      p.row_ml[(int64_t)row.call_row * kChunk * p.Hq + g * p.rep + h] = make_float2(m, inv);
     for (int sp = 0; sp < ns; ++sp)
       wml[sp * p.rep + h].x = exp2f(wml[sp * p.rep + h].x - m) * inv;
   }

@@ -137,6 +137,9 @@ struct kv_cache {
   float *ppart_o = nullptr;
   float2 *ppart_ml = nullptr;
   int64_t ppart_cap = 0;  // vectors
+  // accumulated weights: (m, 1 / l) of the query vectors of a sub-chunk, [B][kChunk][Hq]
+  // (caches with a global layer)
+  float2 *ml = nullptr;
   // host-buffer entry point staging
   void *stage = nullptr;
   size_t stage_bytes = 0;
@@ -516,6 +519,7 @@ void fill_decode(const kv_cache *c, int layer, const __nv_bfloat16 *q, const __n
   dp.early_kv = 0;
   dp.list = nullptr;
   dp.scores = nullptr;
+  dp.row_ml = nullptr;
   dp.tmap_k2 = hybrid ? c->tmRK[layer] : c->tmK[layer];
   dp.tmap_v2 = hybrid ? c->tmRV[layer] : c->tmV[layer];
   dp.k_new2 = k_local;
@@ -681,14 +685,65 @@ int launch_append_rows(kv_cache *c, int layer, const __nv_bfloat16 *k, const __n
   return KV_OK;
 }
 
+// A call that counts its tokens' attention weights (kv_append_weights): per call row the first
+// counted token.
+struct Counted {
+  const float *acc_in;
+  float *acc_out;
+  const std::vector<int32_t> *t0;
+};
+
+// acc_out += the weights of rows `in`, whose attention has left (m, 1 / l) in c->ml.
+int launch_weight_rows(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
+                       const std::vector<WeightsRow> &in, const Counted &cnt, cudaStream_t s) {
+  static thread_local WeightsParams p;
+  const int Hq = c->Hq, Hk = c->Hk, D = c->D;
+  p.K = (const __nv_bfloat16 *)c->K[layer];
+  p.q = q;
+  p.q_row_stride = (int64_t)C * Hq * D;
+  p.rope = c->rope;
+  p.ml = c->ml;
+  p.acc_in = cnt.acc_in;
+  p.acc_out = cnt.acc_out;
+  p.acc_stride = c->max_len;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rep = Hq / Hk;
+  p.D = D;
+  p.seg_rows = c->seg_rows[layer];
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  p.pt = page_table(c, layer);
+  constexpr int kKeys = kWeightTile * kWeightTiles;  // per CTA
+  for (size_t r0 = 0; r0 < in.size(); r0 += kMaxRowsPerLaunch) {
+    const size_t r1 = std::min(in.size(), r0 + kMaxRowsPerLaunch);
+    double bytes = 0, fl = 0;
+    p.n_items = 0;
+    for (size_t j = r0; j < r1; ++j) {
+      WeightsRow &r = p.rows[j - r0];
+      r = in[j];
+      r.item0 = p.n_items;
+      const int keys = r.slots + r.t1;
+      p.n_items += (keys + kKeys - 1) / kKeys;
+      bytes += keys * (2.0 * D + 8.0) * Hk;
+      fl += 2.0 * keys * (double)(r.t1 - r.t0) * Hq * D;
+    }
+    p.n_rows = (int)(r1 - r0);
+    const cudaError_t e =
+        timed(c, KV_KERNEL_WEIGHTS, bytes, fl, s, [&] { return launch_weights(p, s, c->pdl); });
+    if (e != cudaSuccess) return KV_ERR_CUDA;
+  }
+  return KV_OK;
+}
+
 // One layer's chunk for rows `cache_rows`.  k, v: the keys and values of the layer
 // storage (a hybrid layer: its group's global keys, nullptr on a local layer); kl, vl: a
-// hybrid layer's own local keys and values (its ring), else nullptr.
+// hybrid layer's own local keys and values (its ring), else nullptr.  cnt: the call counts its
+// tokens' weights (a global layer; the call has no single-token rows).
 int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                   const __nv_bfloat16 *v, int C, const int32_t *n_new,
                   const std::vector<int32_t> &cache_rows, int Bs, __nv_bfloat16 *out,
                   cudaStream_t s, const __nv_bfloat16 *kl = nullptr,
-                  const __nv_bfloat16 *vl = nullptr) {
+                  const __nv_bfloat16 *vl = nullptr, const Counted *cnt = nullptr) {
   const bool sliding = c->kind[layer] == KV_SLIDING, hybrid = is_hybrid(c->kind[layer]);
   const bool writes_global = c->kind[layer] != KV_HYBRID_LOCAL;  // appends k, v anywhere
   c->cur_layer = layer;
@@ -797,6 +852,7 @@ int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfl
         pp.seg_rows2 = c->R + 1;
         pp.part_o = c->ppart_o;
         pp.part_ml = c->ppart_ml;
+        pp.ml_out = cnt ? c->ml : nullptr;
         int cta = 0;
         double bytes = 0, fl = 0;
         for (size_t j = r0; j < r1; ++j) {
@@ -830,6 +886,7 @@ int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfl
       static thread_local MergeParams mg;
       mg.part_o = c->ppart_o;
       mg.part_ml = c->ppart_ml;
+      mg.ml_out = cnt ? c->ml : nullptr;
       mg.out = out + (int64_t)off * Hq * D;
       mg.out_row_stride = q_row;
       mg.Hq = Hq;
@@ -849,6 +906,18 @@ int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfl
       cudaError_t e = timed(c, KV_KERNEL_COMBINE, mb, 0, s,
                             [&] { return launch_prefill_merge(mg, D, s, c->pdl); });
       if (e != cudaSuccess) return KV_ERR_CUDA;
+    }
+    if (cnt) {  // the weights of the sub-chunk's counted tokens
+      std::vector<WeightsRow> counted;
+      for (const PrefillRow &r : prows) {
+        const int t0 = (*cnt->t0)[r.call_row], slots = slots_of(c, r.cache_row);
+        if (t0 >= off + r.n) continue;
+        const bool first = t0 >= off;
+        counted.push_back({r.cache_row, r.call_row, slots, r.shift, off, std::max(t0, off),
+                           off + r.n, first ? slots : slots + off, first ? 1 : 0, 0});
+      }
+      const int rc = launch_weight_rows(c, layer, q, C, counted, *cnt, s);
+      if (rc != KV_OK) return rc;
     }
     if (ringed) {
       for (size_t r0 = 0; r0 < prows.size(); r0 += kMaxRowsPerLaunch) {
@@ -927,6 +996,7 @@ void free_all(kv_cache *c) {
   cudaFree(c->part_ml);
   cudaFree(c->ppart_o);
   cudaFree(c->ppart_ml);
+  cudaFree(c->ml);
   cudaFree(c->stage);
   cudaFree(c->table);
   for (int8_t *p : c->sparse.bound) cudaFree(p);
@@ -1124,6 +1194,9 @@ static int create_impl(kv_cache **out, int B, int max_len, int Hq, int Hk, int D
   if (!alloc((void **)&c->ppart_o, (size_t)c->ppart_cap * D * 4) ||
       !alloc((void **)&c->ppart_ml, (size_t)c->ppart_cap * 8))
     return fail(KV_ERR_OOM);
+  for (int k : c->kind)
+    if (k == KV_GLOBAL && !c->ml && !alloc((void **)&c->ml, (size_t)B * kChunk * Hq * 8))
+      return fail(KV_ERR_OOM);
   if (cudaDeviceSynchronize() != cudaSuccess) return fail(KV_ERR_CUDA);
   if (const char *pdl = std::getenv("KVINC_PDL")) c->pdl = pdl[0] != '0';
   if (const char *log = std::getenv("KVINC_LOG")) {
@@ -2366,6 +2439,7 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
   dp.list = sp.list;
   dp.list_stride = sp.max_select;
   dp.scores = nullptr;
+  dp.row_ml = nullptr;
   dp.list_sink = sink;
   dp.list_recent = recent;
   static const int no_ring[kMaxRowsPerLaunch] = {};
@@ -2538,159 +2612,50 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
 // ---------------------------------------------------------------- attention weights
 namespace {
 
-// A row of an accumulating call: its tokens and the first counted one.
-struct WeightsIn {
-  int cache_row, call_row, n, t0;
+// A single-token row of a counting call.
+struct SingleIn {
+  int cache_row, call_row;
 };
 
-// Tokens of a row whose query vectors are handled together.
-constexpr int kWeightGroup = kChunk;
-
-// acc_out = acc_in + the weights of the rows' counted tokens, whose keys are appended.
-// Tokens are taken in groups of at most kWeightGroup per row; the first group starts from
-// acc_in, the others add to acc_out.  Rows are batched so that pass 1's partials, one (m, l)
-// per query vector and key split, fit the prefill partials' reserve.
-int accumulate_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
-                       const std::vector<WeightsIn> &in, const float *acc_in, float *acc_out,
-                       cudaStream_t s) {
-  static thread_local WeightsParams p;
-  const int Hq = c->Hq, Hk = c->Hk, D = c->D, rep = Hq / Hk;
-  const int64_t cap = c->ppart_cap;
-  const int group = (int)std::min<int64_t>(kWeightGroup, cap / Hq);
-  p.K = (const __nv_bfloat16 *)c->K[layer];
-  p.q = q;
-  p.q_row_stride = (int64_t)C * Hq * D;
-  p.rope = c->rope;
-  p.part_ml = c->ppart_ml;
-  p.rotated = (__nv_bfloat16 *)c->ppart_o;
-  p.acc_out = acc_out;
-  p.acc_stride = c->max_len;
-  p.Hq = Hq;
-  p.Hk = Hk;
-  p.rep = rep;
-  p.D = D;
-  p.seg_rows = c->seg_rows[layer];
-  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
-  p.pt = page_table(c, layer);
-  const auto tiles = [](int keys) { return (keys + kWeightTile - 1) / kWeightTile; };
-  int most = 0;
-  for (const WeightsIn &w : in) most = std::max(most, w.n - w.t0);
-  for (int g0 = 0; g0 < most; g0 += group) {
-    std::vector<WeightsRow> rows;
-    for (const WeightsIn &w : in) {
-      if (w.n - w.t0 <= g0) continue;
-      WeightsRow r = {};
-      r.cache_row = w.cache_row;
-      r.call_row = w.call_row;
-      r.slots = slots_of(c, w.cache_row);
-      r.shift = c->dropped[w.cache_row];
-      r.n = w.n;
-      r.t0 = w.t0 + g0;
-      r.t1 = std::min(w.n, r.t0 + group);
-      r.first = g0 == 0 ? 1 : 0;
-      rows.push_back(r);
-    }
-    for (size_t r0 = 0; r0 < rows.size();) {
-      // as many rows as the partials hold at one split each
-      size_t r1 = r0;
-      int64_t vecs = 0, work = 0;
-      const auto eights = [&](const WeightsRow &r) { return ((r.t1 - r.t0) * rep + 7) / 8; };
-      while (r1 < rows.size() && r1 - r0 < (size_t)kMaxRowsPerLaunch) {
-        const int64_t v = (int64_t)(rows[r1].t1 - rows[r1].t0) * Hq;
-        if (vecs + v > cap) break;
-        vecs += v;
-        work += (int64_t)tiles(rows[r1].slots + rows[r1].n) * eights(rows[r1]);
-        ++r1;
-      }
-      // A CTA's work is its key tiles times the query vectors (in eights).  Two CTAs are
-      // resident per SM: splits of about an equal share of them, at least four tiles, and
-      // longer ones while the launch would need a second wave or the partials do not fit.
-      const int64_t slots2 = 2LL * c->num_sms;
-      for (int64_t share = (work * Hk + slots2 - 1) / slots2;; share += (share + 7) / 8) {
-        int64_t part = 0;
-        int item = 0;
-        bool more = false;  // a row is still split
-        for (size_t j = r0; j < r1; ++j) {
-          WeightsRow &r = p.rows[j - r0];
-          r = rows[j];
-          const int nt = tiles(r.slots + r.t1);
-          const int64_t per = std::max<int64_t>(4, (share + eights(r) - 1) / eights(r));
-          r.split_tiles = (int)std::min<int64_t>(per, nt);
-          r.n_splits = (nt + r.split_tiles - 1) / r.split_tiles;
-          more |= r.n_splits > 1;
-          r.item0 = item;
-          r.part = (int32_t)part;
-          item += r.n_splits;
-          part += (int64_t)r.n_splits * (r.t1 - r.t0) * Hq;
-        }
-        p.n_items = item;
-        if (!more || (part <= cap && (int64_t)item * Hk <= slots2)) break;
-      }
-      p.n_rows = (int)(r1 - r0);
-      double kb = 0, fl = 0;
-      for (int j = 0; j < p.n_rows; ++j) {
-        const WeightsRow &r = p.rows[j];
-        kb += 2.0 * (r.slots + r.t1) * Hk * D;
-        fl += 2.0 * (r.slots + r.t1) * (double)(r.t1 - r.t0) * Hq * D;
-      }
-      p.acc_in = g0 == 0 ? acc_in : acc_out;
-      cudaError_t e = timed(c, KV_KERNEL_WEIGHTS, kb, fl, s,
-                            [&] { return launch_weights(p, 1, s, c->pdl); });
-      if (e != cudaSuccess) return KV_ERR_CUDA;
-      // pass 2: CTAs over every slot that the call defines
-      int item = 0;
-      double ab = 0;
-      for (int j = 0; j < p.n_rows; ++j) {
-        WeightsRow &r = p.rows[j];
-        r.item0 = item;
-        item += (tiles(r.slots + r.n) + kWeightSumTiles - 1) / kWeightSumTiles;
-        ab += 8.0 * (r.slots + r.n) * Hk;
-      }
-      p.n_items = item;
-      e = timed(c, KV_KERNEL_WEIGHTS, kb + ab, fl, s,
-                [&] { return launch_weights(p, 2, s, c->pdl); });
-      if (e != cudaSuccess) return KV_ERR_CUDA;
-      r0 = r1;
-    }
-  }
-  return KV_OK;
-}
-
-// Append, attention and weights of single-token rows in one pass over their keys: decode
-// launches that store the scores in the prefill partials' reserve, each followed by the
-// join.  `in` holds the rows whose scores fit; a launch takes as many as fit together, all
-// launches about equally many.
-int decode_with_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
-                        const __nv_bfloat16 *v, int C, const std::vector<WeightsIn> &in,
-                        const float *acc_in, float *acc_out, __nv_bfloat16 *out,
-                        cudaStream_t s) {
+// Append, attention and weights of single-token rows.  With `store` in one pass over their
+// keys: decode launches that store the scores in the prefill partials' reserve, each followed
+// by the join; a launch takes as many rows as fit there together, all launches about equally
+// many.  Without, for rows whose scores alone are too many, the weights take a pass over K.
+int decode_counted(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
+                   const __nv_bfloat16 *v, int C, const std::vector<SingleIn> &in, bool store,
+                   const Counted &cnt, __nv_bfloat16 *out, cudaStream_t s) {
+  if (in.empty()) return KV_OK;
   static thread_local DecodeParams dp;
   static thread_local JoinParams jp;
   int longest = 0;
-  for (const WeightsIn &w : in) longest = std::max(longest, slots_of(c, w.cache_row) + 1);
+  for (const SingleIn &w : in) longest = std::max(longest, slots_of(c, w.cache_row) + 1);
   const int64_t stride = (longest + 3) / 4 * 4;
-  const int64_t room = c->ppart_cap * c->D / (c->Hq * stride);
-  const size_t most = (size_t)std::min<int64_t>(
-      std::min<int64_t>(room, c->ppart_cap / c->Hq), kMaxRowsPerLaunch);
+  const int64_t room = store ? c->ppart_cap * c->D / (c->Hq * stride) : kMaxRowsPerLaunch;
+  const size_t most = (size_t)std::min<int64_t>(room, kMaxRowsPerLaunch);
   const size_t launches = (in.size() + most - 1) / most;
   const size_t per = (in.size() + launches - 1) / launches;
   for (size_t r0 = 0; r0 < in.size(); r0 += per) {
     const size_t r1 = std::min(in.size(), r0 + per);
     std::vector<DecodeIn> batch;
+    std::vector<WeightsRow> pass;
     jp.n_items = 0;
     double ab = 0;
     for (size_t j = r0; j < r1; ++j) {
       const int r = in[j].cache_row, slot = slots_of(c, r);
       batch.push_back({r, in[j].call_row, c->lens[r], slot});
-      jp.rows[j - r0] = {r, slot + 1, jp.n_items};
-      jp.n_items += (slot + kJoinSlots) / kJoinSlots;
-      ab += (slot + 1.0) * (8.0 * c->Hk + 4.0 * c->Hq);
+      if (store) {
+        jp.rows[j - r0] = {r, in[j].call_row, slot + 1, jp.n_items};
+        jp.n_items += (slot + kJoinSlots) / kJoinSlots;
+        ab += (slot + 1.0) * (8.0 * c->Hk + 4.0 * c->Hq);
+      } else {
+        pass.push_back({r, in[j].call_row, slot, c->dropped[r], 0, 0, 1, slot, 1, 0});
+      }
     }
     double bytes = 0, fl = 0;
     fill_decode(c, layer, q, k, v, out, (int64_t)C * c->Hq * c->D, (int64_t)C * c->Hk * c->D,
                 batch, dp, bytes, fl);
-    dp.scores = c->ppart_o;
-    dp.row_ml = c->ppart_ml;
+    dp.scores = store ? c->ppart_o : nullptr;
+    dp.row_ml = c->ml;
     dp.score_stride = stride;
     dp.early_kv = early_kv_ok(c, layer, s) ? 1 : 0;
     if (!c->pdl) dp.deep_pipeline = 0;
@@ -2698,11 +2663,16 @@ int decode_with_weights(kv_cache *c, int layer, const __nv_bfloat16 *q, const __
       return launch_decode(dp, c->D, c->Hq / c->Hk <= 8 ? 1 : 2, s, c->pdl);
     });
     if (e != cudaSuccess) return KV_ERR_CUDA;
+    if (!store) {
+      const int rc = launch_weight_rows(c, layer, q, C, pass, cnt, s);
+      if (rc != KV_OK) return rc;
+      continue;
+    }
     jp.scores = c->ppart_o;
-    jp.row_ml = c->ppart_ml;
+    jp.row_ml = c->ml;
     jp.score_stride = stride;
-    jp.acc_in = acc_in;
-    jp.acc_out = acc_out;
+    jp.acc_in = cnt.acc_in;
+    jp.acc_out = cnt.acc_out;
     jp.acc_stride = c->max_len;
     jp.Hq = c->Hq;
     jp.Hk = c->Hk;
@@ -2726,46 +2696,44 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
   std::vector<int32_t> cache_rows;
   int rc = check_rows(c, n_new, rows, Bs, C, cache_rows);
   if (rc != KV_OK) return rc;
-  // Single-token rows take one pass over their keys while a row's scores fit the reserve; the
-  // rest take their attention as kv_append gives it and then two passes over K.
-  std::vector<WeightsIn> single, in;
-  std::vector<int32_t> n_rest(n_new, n_new + std::max(Bs, 0));
+  // Single-token rows apart: in one pass over their keys while a row's scores fit the reserve.
+  std::vector<SingleIn> stored, longer;
+  std::vector<int32_t> n_rest(n_new, n_new + std::max(Bs, 0)), t0(std::max(Bs, 0), 0);
   std::vector<std::pair<int, int>> want;
+  bool chunks = false;
   for (int i = 0; i < Bs; ++i) {
     if (n_new[i] == 0) continue;
-    const WeightsIn w = {cache_rows[i], i, n_new[i], n_new[i] - std::min(n_new[i], last)};
-    const int64_t stride = (slots_of(c, cache_rows[i]) + 1 + 3) / 4 * 4;
-    want.push_back({cache_rows[i], slots_of(c, cache_rows[i]) + n_new[i]});
-    if (n_new[i] == 1 && stride * c->Hq <= c->ppart_cap * c->D && c->Hq <= c->ppart_cap) {
-      single.push_back(w);
-      n_rest[i] = 0;
-    } else {
-      in.push_back(w);
+    const int slots = slots_of(c, cache_rows[i]);
+    want.push_back({cache_rows[i], slots + n_new[i]});
+    t0[i] = n_new[i] - std::min(n_new[i], last);
+    if (n_new[i] > 1) {
+      chunks = true;
+      continue;
     }
+    const int64_t stride = (slots + 1 + 3) / 4 * 4;
+    (stride * Hq <= c->ppart_cap * c->D ? stored : longer).push_back({cache_rows[i], i});
+    n_rest[i] = 0;
   }
   if (want.empty()) return KV_OK;
   if (!q || !k || !v || !out || !acc_in || !acc_out || !aligned16(q) || !aligned16(k) ||
       !aligned16(v) || !aligned16(out) ||
       ((reinterpret_cast<uintptr_t>(acc_in) | reinterpret_cast<uintptr_t>(acc_out)) & 3u))
     return KV_ERR_ARG;
-  if (Hq > c->ppart_cap) return KV_ERR_SCRATCH;
   DeviceGuard guard(c->device);
   cudaStream_t s = (cudaStream_t)stream;
   rc = ensure_blocks(c, want, s);  // every row's, before anything else is enqueued
   if (rc != KV_OK) return rc;
   c->cur_layer = layer;
-  if (!single.empty()) {
-    rc = decode_with_weights(c, layer, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)k,
-                             (const __nv_bfloat16 *)v, C, single, acc_in, acc_out,
-                             (__nv_bfloat16 *)out, s);
-    if (rc != KV_OK) return rc;
-  }
-  if (in.empty()) return KV_OK;
-  rc = append_device(c, layer, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)k,
-                     (const __nv_bfloat16 *)v, C, n_rest.data(), cache_rows, Bs,
-                     (__nv_bfloat16 *)out, s);
-  if (rc != KV_OK) return rc;
-  return accumulate_weights(c, layer, (const __nv_bfloat16 *)q, C, in, acc_in, acc_out, s);
+  const __nv_bfloat16 *qb = (const __nv_bfloat16 *)q, *kb = (const __nv_bfloat16 *)k;
+  const __nv_bfloat16 *vb = (const __nv_bfloat16 *)v;
+  __nv_bfloat16 *ob = (__nv_bfloat16 *)out;
+  const Counted cnt = {acc_in, acc_out, &t0};
+  rc = decode_counted(c, layer, qb, kb, vb, C, stored, true, cnt, ob, s);
+  if (rc == KV_OK) rc = decode_counted(c, layer, qb, kb, vb, C, longer, false, cnt, ob, s);
+  if (rc == KV_OK && chunks)
+    rc = append_device(c, layer, qb, kb, vb, C, n_rest.data(), cache_rows, Bs, ob, s, nullptr,
+                       nullptr, &cnt);
+  return rc;
 } catch (...) {  // host memory
   return KV_ERR_OOM;
 }

@@ -174,9 +174,10 @@ struct DecodeParams {  // 64-byte aligned through its CUtensorMap members
   // nullptr: tile t is slots [64 t, 64 t + 64).
   const int32_t *list;
   int list_stride, list_sink, list_recent;
-  // Accumulated weights (the scores variant): head hq's score of slot j, in log2 units, goes
-  // to scores[(r * Hq + hq) * score_stride + j] for row r of the launch, and the softmax
-  // maximum and the reciprocal of its sum to row_ml[r * Hq + hq].  nullptr: neither.
+  // Accumulated weights (the scores variant, row_ml set): head hq's softmax maximum (log2
+  // units; any reference the sum is taken from) and the reciprocal of its sum go to
+  // row_ml[call_row * kChunk * Hq + hq] and, unless scores is nullptr, its score of slot j, in
+  // log2 units, to scores[(r * Hq + hq) * score_stride + j] for row r of the launch.
   float *scores;
   float2 *row_ml;
   int64_t score_stride;
@@ -228,6 +229,9 @@ struct PrefillParams {  // 64-byte aligned through its CUtensorMap members
   // key splits: [vector][D] fp32 O (relative to m), [vector] (m in log2 units, l)
   float *part_o;
   float2 *part_ml;
+  // accumulated weights: (m, 1 / l) of token t of the sub-chunk and head hq of an entry that
+  // covers all keys go to ml_out[(call_row * kChunk + t) * Hq + hq]; nullptr: nowhere
+  float2 *ml_out;
   PrefillRow rows[kMaxRowsPerLaunch];
 };
 
@@ -251,6 +255,7 @@ struct MergeParams {
   const float2 *part_ml;
   __nv_bfloat16 *out;       // offset to the sub-chunk
   int64_t out_row_stride;
+  float2 *ml_out;           // as PrefillParams::ml_out, of the merged rows
   int Hq, Hk, rep;
   int n_rows, n_vec;
   MergeRow rows[kMaxRowsPerLaunch];
@@ -365,31 +370,28 @@ struct SelectParams {
 };
 
 // ---------------------------------------------------------------- attention weights
-// Per key of a row, the softmax weights that the counted query tokens [t0, n) of a call
-// give it, summed over them and over the kv head's query heads.  Pass 1 finds every query
-// vector's softmax maximum and sum over the row's keys, in parts per key split; pass 2 sums
-// the weights per key.  Query vectors are numbered (t - t0) * rep + head.
+// Per key of a row, the softmax weights that the counted tokens [t0, t1) of one sub-chunk give
+// it, summed over them and over the kv head's query heads; the attention kernels have left
+// every query vector's (m, 1 / l).
 struct WeightsRow {
   int32_t cache_row;
   int32_t call_row;
-  int32_t slots;    // keys before the call; token t sits at slot slots + t
+  int32_t slots;    // keys before the call; token t of the call sits at slot slots + t
   int32_t shift;    // a token's position minus its slot
-  int32_t n;        // tokens of the call, all appended
-  int32_t t0, t1;   // counted tokens
-  int32_t first;    // 1: acc_in holds the accumulator of slots below `slots`; 0: of all slots
-  int32_t item0;    // first CTA (key split / key tile) of this row in the launch
-  int32_t n_splits, split_tiles;  // of pass 1, in kWeightTile keys
-  int32_t part;     // first (m, l) vector of the row
+  int32_t tok0;     // first token of the sub-chunk
+  int32_t t0, t1;   // counted tokens of it
+  int32_t known;    // slots below it have an accumulator; the others start at 0
+  int32_t first;    // 1: that accumulator is in acc_in, 0: in acc_out
+  int32_t item0;    // first CTA of this row in the launch
 };
 constexpr int kWeightTile = 128;   // keys per CTA and step
-constexpr int kWeightSumTiles = 4;  // tiles per CTA of pass 2
+constexpr int kWeightTiles = 4;    // tiles per CTA
 struct WeightsParams {
   const __nv_bfloat16 *K;  // layer storage
   const __nv_bfloat16 *q;  // [Bs][C][Hq][D]
   int64_t q_row_stride;
   const float2 *rope;
-  float2 *part_ml;         // [part + (split * Hk + g) * n_vec + vec]: max (log2 units), sum
-  __nv_bfloat16 *rotated;  // [part + g * n_vec + vec][D]: the rotated query vectors
+  const float2 *ml;        // [(call_row * kChunk + t - tok0) * Hq + head]: m (log2 units), 1 / l
   const float *acc_in;     // [B][Hk][acc_stride]
   float *acc_out;
   int acc_stride;
@@ -404,13 +406,14 @@ struct WeightsParams {
 // launch has `keys` slots, the last of them its new token's.
 struct JoinRow {
   int32_t cache_row;
+  int32_t call_row;
   int32_t keys;
   int32_t item0;  // first CTA (kJoinSlots slots) of this row
 };
 constexpr int kJoinSlots = 1024;
 struct JoinParams {
   const float *scores;     // [row of the launch][Hq][score_stride]
-  const float2 *row_ml;    // [row][Hq]
+  const float2 *row_ml;    // as DecodeParams::row_ml
   int64_t score_stride;
   const float *acc_in;     // [B][Hk][acc_stride]
   float *acc_out;
@@ -496,7 +499,7 @@ cudaError_t launch_commit(const CommitParams &p, cudaStream_t s, bool pdl = fals
 cudaError_t launch_state(const StateParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_bounds(const BoundsParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_select(const SelectParams &p, cudaStream_t s, bool pdl = false);
-cudaError_t launch_weights(const WeightsParams &p, int pass, cudaStream_t s, bool pdl = false);
+cudaError_t launch_weights(const WeightsParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_join(const JoinParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t s, bool pdl = false);
 cudaError_t launch_evict_move(const EvictParams &p, bool in_place, cudaStream_t s,

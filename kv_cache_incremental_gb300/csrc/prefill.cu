@@ -380,6 +380,9 @@ __global__ void __launch_bounds__(kThreads) prefill_kernel(const __grid_constant
     __nv_bfloat16 *dst = p.out + (int64_t)row.call_row * p.out_row_stride +
                          ((int64_t)t * p.Hq + g * p.rep + h) * D;
     const float inv = 1.f / l_run[rj];
+    if (p.ml_out && qq == 0)
+      p.ml_out[((int64_t)row.call_row * kChunk + t) * p.Hq + g * p.rep + h] =
+          make_float2(m_run[rj], inv);
 #pragma unroll
     for (int nd = 0; nd < D / 8; ++nd) {
       const float x0 = o[nd][2 * rj] * inv, x1 = o[nd][2 * rj + 1] * inv;
@@ -456,6 +459,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int t = rho / p.rep, h = rho % p.rep;
+  if (p.ml_out && lane == 0)
+    p.ml_out[((int64_t)row.call_row * kChunk + t) * p.Hq + g * p.rep + h] =
+        make_float2(m_max, inv);
   __nv_bfloat16 *dst = p.out + (int64_t)row.call_row * p.out_row_stride +
                        ((int64_t)t * p.Hq + g * p.rep + h) * D + kPer * lane;
   if (kPer == 4) {

@@ -765,6 +765,9 @@ __global__ void __launch_bounds__(Roles<TQ>::kThreads, TQ == 1 ? 2 : 1)
         tc::fence_after();
         const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
         const int t = qvalid ? rho / p.rep : 0, h = qvalid ? rho % p.rep : 0;
+        if (p.ml_out && qvalid)
+          p.ml_out[((int64_t)row.call_row * kChunk + t) * p.Hq + g * p.rep + h] =
+              make_float2(m_used, inv);
         __nv_bfloat16 *dst = p.out + (int64_t)row.call_row * p.out_row_stride +
                              ((int64_t)t * p.Hq + g * p.rep + h) * D;
 #pragma unroll 1  // one 16-column chunk of code (instruction fetch)

@@ -17,12 +17,21 @@ def test_a_row_of_a_million_keys():
     r.cache.enable_sparse(310)
     test_sparse.step(r, [1], 2, 300, 8)                 # 16382 candidate blocks
     test_weights.step(r, [1])                           # one pass: the scores fit
-    test_weights.step(r, [3], 2)                        # two passes
+    test_weights.step(r, [3], 2)                        # a chunk: one more pass over K
     test_evict.evict(r, r, [0], [0], 5000, 64)          # weights past shared memory
     test_evict.check_state(r)
     assert r.cache.lens == [L + 5] and r.cache.slots == [5000]
     test_sparse.step(r, [1], 1, 3, 2)                   # positions at the rotary table's end
     test_weights.step(r, [1])
+    assert r.cache.device_error() == 0
+
+
+def test_rows_whose_scores_outgrow_their_room():
+    """64 heads' scores of 330000 keys are more than a cache reserves room for: that row's
+    weights take a pass of their own, beside a row and a chunk that go the usual ways."""
+    r = Rows(3, 1 << 20, 64, 4, 64, [330000, 500, 70], seed=5)
+    test_weights.step(r, [1, 1, 3])
+    test_weights.step(r, [1, 0, 1], inplace=True)
     assert r.cache.device_error() == 0
 
 
