@@ -713,7 +713,7 @@ int launch_weight_rows(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
   p.seg_rows = c->seg_rows[layer];
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
   p.pt = page_table(c, layer);
-  constexpr int kKeys = kWeightTile * kWeightTiles;  // per CTA
+  const int per_cta = kWeightTile * (D == 64 ? kWeightTiles<64> : kWeightTiles<128>);
   for (size_t r0 = 0; r0 < in.size(); r0 += kMaxRowsPerLaunch) {
     const size_t r1 = std::min(in.size(), r0 + kMaxRowsPerLaunch);
     double bytes = 0, fl = 0;
@@ -723,7 +723,7 @@ int launch_weight_rows(kv_cache *c, int layer, const __nv_bfloat16 *q, int C,
       r = in[j];
       r.item0 = p.n_items;
       const int keys = r.slots + r.t1;
-      p.n_items += (keys + kKeys - 1) / kKeys;
+      p.n_items += (keys + per_cta - 1) / per_cta;
       bytes += keys * (2.0 * D + 8.0) * Hk;
       fl += 2.0 * keys * (double)(r.t1 - r.t0) * Hq * D;
     }

@@ -384,8 +384,9 @@ struct WeightsRow {
   int32_t first;    // 1: that accumulator is in acc_in, 0: in acc_out
   int32_t item0;    // first CTA of this row in the launch
 };
-constexpr int kWeightTile = 128;   // keys per CTA and step
-constexpr int kWeightTiles = 4;    // tiles per CTA
+constexpr int kWeightTile = 128;  // keys per CTA and step
+template <int D>
+constexpr int kWeightTiles = D == 64 ? 2 : 4;  // tiles per CTA (weights_kernel: why)
 struct WeightsParams {
   const __nv_bfloat16 *K;  // layer storage
   const __nv_bfloat16 *q;  // [Bs][C][Hq][D]

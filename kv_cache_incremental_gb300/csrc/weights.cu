@@ -188,10 +188,16 @@ __device__ __forceinline__ void sum_step(const uint4 (&f)[D / 16], const uint8_t
   }
 }
 
-// One CTA per (row, kWeightTiles tiles of 128 keys, kv head).
+// One CTA per (row, kWeightTiles tiles of 128 keys, kv head).  Bound by instruction issue (per
+// 16 keys and 8 vectors D / 16 MMAs, 4 ex2 and about 20 others), so by the warps to issue from.
+// D = 64: two tiles leave room for three CTAs per SM: 126.1 us for a call (24 rows, chunks of up
+// to 64 tokens, the last 32 counted, Hq 16, Hk 4); four tiles and two CTAs 128.9, two and two
+// 130.7, four and three (spilling) 139.1.  D = 128: two CTAs by its registers, where more tiles
+// read the queries less often: four 65.0 us, two 69.1 (24 rows of 6k keys, 8 counted, Hq 32).
 template <int D>
-__global__ void __launch_bounds__(kWThreads, 2)
+__global__ void __launch_bounds__(kWThreads, D == 64 ? 3 : 2)
     weights_kernel(const __grid_constant__ WeightsParams p) {
+  constexpr int kTiles = kWeightTiles<D>;
   __shared__ __align__(16) uint8_t qs[8 * QT * kQStride<D>];
   __shared__ __align__(16) float2 ml[8 * QT];
   __shared__ int limit[8 * QT];
@@ -200,12 +206,12 @@ __global__ void __launch_bounds__(kWThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, qq = lane & 3;
   const int n_vec = (row.t1 - row.t0) * p.rep;
   const int keys = row.slots + row.t1;  // slots whose accumulator the launch defines
-  const int kb0 = ((int)blockIdx.x - row.item0) * kWeightTiles * kWeightTile + 16 * warp;
+  const int kb0 = ((int)blockIdx.x - row.item0) * kTiles * kWeightTile + 16 * warp;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  float sum[kWeightTiles][2];
+  float sum[kTiles][2];
 #pragma unroll
-  for (int i = 0; i < kWeightTiles; ++i) sum[i][0] = sum[i][1] = 0.f;
+  for (int i = 0; i < kTiles; ++i) sum[i][0] = sum[i][1] = 0.f;
   for (int v0 = 0; v0 < n_vec; v0 += 8 * QT) {
     const int n_nt = min(QT, (n_vec - v0 + 7) / 8);
     uint4 a[D / 32], b[D / 32];
@@ -214,12 +220,12 @@ __global__ void __launch_bounds__(kWThreads, 2)
     load_queries<D>(p, row, g, v0, n_vec, qs, ml, limit);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWeightTiles; ++i) {
+    for (int i = 0; i < kTiles; ++i) {
       const int kb = kb0 + i * kWeightTile;
       if (kb >= keys) break;
       uint4 f[D / 16];
       fragments<D>(a, b, f);
-      if (i + 1 < kWeightTiles && kb + kWeightTile < keys)  // the next keys, meanwhile
+      if (i + 1 < kTiles && kb + kWeightTile < keys)  // the next keys, meanwhile
         load_keys<D>(p, row, g, kb + kWeightTile, keys - 1, lane, a, b);
       if (kb + 15 <= row.slots + row.t0)
         sum_step<D, true>(f, qs, limit, ml, n_nt, kb + gq, p.scale_log2, lane, sum[i][0],
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
   }
   const float *before = row.first ? p.acc_in : p.acc_out;
 #pragma unroll
-  for (int i = 0; i < kWeightTiles; ++i) {
+  for (int i = 0; i < kTiles; ++i) {
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
       sum[i][0] += __shfl_xor_sync(0xffffffffu, sum[i][0], off);
