@@ -2578,8 +2578,13 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
     rc = update_bounds(c, layer, live, slots, kept, s);
     if (rc != KV_OK) return rc;
   }
-  // queries in launches of at most kMaxRowsPerLaunch, whose tokens lie within 2^16 of the
+  // queries in launches of at most kMaxRowsPerLaunch, all about equally many (571 queries as
+  // 512 and 59: 86.4 us for the call, as 286 and 285: 79.2), whose tokens lie within 2^16 of the
   // first one's (the kernels' 16-bit token index)
+  int64_t total = 0;
+  for (int i = 0; i < Bs; ++i) total += n_new[i];
+  const int64_t launches = (total + kMaxRowsPerLaunch - 1) / kMaxRowsPerLaunch;
+  const int64_t most = (total + launches - 1) / launches;
   std::vector<SelectQuery> batch;
   const auto flush = [&]() -> int {
     return attend_selected(c, layer, (const __nv_bfloat16 *)q, fused ? kb : nullptr,
@@ -2590,7 +2595,7 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
     for (int t = 0; t < n_new[i]; ++t) {
       const int r = cache_rows[i], slot = slots_of(c, r) + t, tok = i * C + t;
       if (!batch.empty() &&
-          ((int)batch.size() == kMaxRowsPerLaunch || tok - batch[0].tok > 0xffff)) {
+          ((int64_t)batch.size() == most || tok - batch[0].tok > 0xffff)) {
         if ((rc = flush()) != KV_OK) return rc;
         batch.clear();
       }
