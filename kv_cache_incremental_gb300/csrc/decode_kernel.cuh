@@ -622,14 +622,15 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
       __syncwarp();
     }
     attend16<D, NT, SCORES, LAZY>(acc, qb, kt, vt, kTileKeys * 128, 16 * warp, n_valid,
-                            skip_here ? skip : -1, p.scale_log2, lane, scores ? scores + key_base : nullptr,
-                            p.score_stride, p.rep);
+                                  skip_here ? skip : -1, p.scale_log2, lane,
+                                  scores ? scores + key_base : nullptr, p.score_stride, p.rep);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&empty[s]);
   }
   if (owner && warp == 0 && !*fail)  // the new key, from the mini-tile (row 0 only)
-    attend16<D, NT, SCORES, LAZY>(acc, qb, mini_k, mini_v, kMiniRows * 128, 0, 1, -1, p.scale_log2, lane,
-                            scores ? scores + new_slot : nullptr, p.score_stride, p.rep);
+    attend16<D, NT, SCORES, LAZY>(acc, qb, mini_k, mini_v, kMiniRows * 128, 0, 1, -1,
+                                  p.scale_log2, lane, scores ? scores + new_slot : nullptr,
+                                  p.score_stride, p.rep);
 
   // ---------------------------------------------------------------- merge warps
   // All consumers are past their last tile before the stage memory is reused.

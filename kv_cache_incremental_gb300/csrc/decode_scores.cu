@@ -1,4 +1,5 @@
-// decode_scores.cu -- the decode kernel's variants that also store every key's scores (accumulated weights).
+// decode_scores.cu -- the decode kernel's variants that also store each head's softmax maximum and
+// sum and, if wanted, every key's scores (accumulated weights).
 #include "decode_kernel.cuh"
 
 namespace kvinc {

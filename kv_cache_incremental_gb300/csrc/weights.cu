@@ -140,16 +140,16 @@ __device__ __forceinline__ void scores(const uint4 (&f)[D / 16], const uint8_t *
       w[i] = *reinterpret_cast<const uint4 *>(qr + 8 * i * kQStride<D> + 64 * j);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const uint4 &x = f[2 * j];
-        if (j == 0)
-          ptx::mma_bf16_zero(s[i], x.x, x.y, x.z, x.w, w[i].x, w[i].y);
-        else
-          ptx::mma_bf16(s[i], x.x, x.y, x.z, x.w, w[i].x, w[i].y);
+      const uint4 &x = f[2 * j];
+      if (j == 0)
+        ptx::mma_bf16_zero(s[i], x.x, x.y, x.z, x.w, w[i].x, w[i].y);
+      else
+        ptx::mma_bf16(s[i], x.x, x.y, x.z, x.w, w[i].x, w[i].y);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const uint4 &x = f[2 * j + 1];
-        ptx::mma_bf16(s[i], x.x, x.y, x.z, x.w, w[i].z, w[i].w);
+      const uint4 &x = f[2 * j + 1];
+      ptx::mma_bf16(s[i], x.x, x.y, x.z, x.w, w[i].z, w[i].w);
     }
   }
 }
