@@ -406,8 +406,9 @@ constexpr int kMergeWarps = 8;
 // One warp per (row, kv head, query row) vector: the log-sum-exp merge of the row's key
 // splits (a split in which the query row sees no key has m = -inf and weighs nothing).
 // Every split's (m, l) and then every split's slice of O are loaded before any is used, so
-// a vector costs two memory round trips whatever its split count.
-template <int D>
+// a vector costs two memory round trips whatever its split count.  COUNTED: the merged (m, 1 / l)
+// go to p.ml_out (a variant: a test of the pointer cost 0.3 of 11 us where there is none).
+template <int D, bool COUNTED>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     prefill_merge_kernel(const __grid_constant__ MergeParams p) {
   ptx::grid_dep_wait();  // the previous grid on the stream has completed
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int t = rho / p.rep, h = rho % p.rep;
-  if (p.ml_out && lane == 0)
+  if (COUNTED && lane == 0)
     p.ml_out[((int64_t)row.call_row * kChunk + t) * p.Hq + g * p.rep + h] =
         make_float2(m_max, inv);
   __nv_bfloat16 *dst = p.out + (int64_t)row.call_row * p.out_row_stride +
@@ -492,9 +493,12 @@ cudaError_t launch_prefill(const PrefillParams &p, int D, cudaStream_t s, bool p
 cudaError_t launch_prefill_merge(const MergeParams &p, int D, cudaStream_t s, bool pdl) {
   if (p.n_vec <= 0) return cudaSuccess;
   const dim3 blocks((p.n_vec + kMergeWarps - 1) / kMergeWarps), threads(kMergeWarps * 32);
-  if (D == 128) return launch_k(prefill_merge_kernel<128>, blocks, threads, 0, s, p, pdl);
-  if (D == 64) return launch_k(prefill_merge_kernel<64>, blocks, threads, 0, s, p, pdl);
-  return cudaErrorInvalidValue;
+  if (D != 128 && D != 64) return cudaErrorInvalidValue;
+  const auto kernel = D == 128 ? (p.ml_out ? prefill_merge_kernel<128, true>
+                                           : prefill_merge_kernel<128, false>)
+                               : (p.ml_out ? prefill_merge_kernel<64, true>
+                                           : prefill_merge_kernel<64, false>);
+  return launch_k(kernel, blocks, threads, 0, s, p, pdl);
 }
 
 cudaError_t configure_prefill() {
