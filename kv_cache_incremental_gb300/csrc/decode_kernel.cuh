@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
   // The item's key segment: 0 = the layer storage (a global cache, a sliding ring, or a
   // hybrid layer's group cache), 1 = a hybrid layer's own ring.
   const int split = item - row.item0;          // over all the row's splits (merge slot)
-  const bool seg1 = split >= row.n_splits;
+  const bool seg1 = !LIST && split >= row.n_splits;
   const int n_total = row.n_splits + row.n_splits2;
   const int ssplit = seg1 ? split - row.n_splits : split;
   const int split_len = (seg1 ? row.split_tiles2 : row.split_tiles) * kTileKeys;
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
   const int n_tiles = (k1 - k0 + kTileKeys - 1) / kTileKeys;
   // a cache's new key comes after the row's others (at slot pos unless keys were evicted)
   const int new_slot = seg1 || p.seg0_ring ? row.pos % p.ring_R : row.nk - 1;
-  const bool owner = (seg1 ? p.fuse_append2 : p.fuse_append) && new_slot >= k0 && new_slot < k1;
+  const bool owner =
+      !LIST && (seg1 ? p.fuse_append2 : p.fuse_append) && new_slot >= k0 && new_slot < k1;
   const int seg_rows = seg1 ? p.seg_rows2 : p.seg_rows;
   PageTable pt = p.pt;
   if (seg1) pt.max_blocks = 0;                 // rings are dense
