@@ -485,7 +485,7 @@ int kv_import_row(kv_cache *c, int row, int keep, const void *src, int64_t bytes
  * kv_sparse_enable: prepares a cache with at least one KV_GLOBAL layer for calls of up to
  *   max_select (1..4096) blocks per query: allocates, for every global layer, the bounds
  *   (2 D + 4 bytes per row, kv head and block of 64: 1/128 of the K/V bytes), and block
- *   lists of 512 x Hk x max_select int32.  Once per cache (KV_ERR_ARG after that),
+ *   lists of 1024 x Hk x max_select int32.  Once per cache (KV_ERR_ARG after that),
  *   KV_ERR_OOM if the memory cannot be had; freed with the cache.  SYNCHRONISES the device.
  * kv_append_sparse: kv_append on a KV_GLOBAL layer (same q, k, v, n_new, rows, out, effects
  *   and errors) with the attention above for every new token.  0 <= sink, 0 <= top_k,

@@ -171,7 +171,7 @@ struct kv_cache {
     std::vector<int8_t *> bound;
     std::vector<float *> scale;
     std::vector<std::vector<int32_t>> valid;  // [layer][row]
-    int32_t *list = nullptr;                  // [kMaxRowsPerLaunch][Hk][max_select]
+    int32_t *list = nullptr;                  // [kMaxSelectQueries][Hk][max_select]
     int32_t *counters = nullptr;              // [kMaxRowsPerLaunch][Hk]
   } sparse;
   // the cache's last kernel launch (stream, kernel kind or -1 for one that may write any
@@ -2358,12 +2358,18 @@ int update_bounds(kv_cache *c, int layer, const std::vector<int32_t> &rows,
   return KV_OK;
 }
 
-// Selection and attention of up to kMaxRowsPerLaunch queries, tokens [tok0, tok0 + 2^16) of
-// the call's q and out [tok][Hq][D].  k, v: the tokens' keys and values [tok][Hk][D] when the
-// selection appends them (the queries are single tokens of different rows), else nullptr.
+// A query token of a sparse call.
+struct SparseQuery {
+  int cache_row, slot, pos, tok;
+  int pend0, n_pend;  // as SelectRow
+};
+
+// Selection and attention of up to kMaxSelectQueries queries of up to kMaxRowsPerLaunch rows.
+// k, v: the tokens' keys and values [tok][Hk][D] when the selection appends them (the queries
+// are single tokens of different rows), else nullptr.
 int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                     const __nv_bfloat16 *v, __nv_bfloat16 *out,
-                    const std::vector<SelectQuery> &qs, int sink, int top_k, int recent,
+                    const std::vector<SparseQuery> &qs, int sink, int top_k, int recent,
                     int32_t *selected, cudaStream_t s) {
   kv_cache::Sparse &sp = c->sparse;
   static thread_local SelectParams p;
@@ -2392,23 +2398,17 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
   p.top_k = top_k;
   p.recent = recent;
   p.n_queries = n;
+  p.n_rows = 0;
   p.max_cand = 0;
-  double sel_bytes = 0, kv_bytes = 0, flops = 0;
-  const int tok0 = qs[0].tok;
+  double sel_bytes = 0;
   for (int i = 0; i < n; ++i) {
-    p.queries[i] = qs[i];
-    const int nb = qs[i].slot / kSparseBlock + 1, n_sel = std::min(nb, per);
+    if (k || i == 0 || qs[i].cache_row != qs[i - 1].cache_row)
+      p.rows[p.n_rows++] = {qs[i].cache_row, qs[i].slot,  qs[i].pos, qs[i].tok,
+                            qs[i].pend0,     qs[i].n_pend, i};
+    const int nb = qs[i].slot / kSparseBlock + 1;
     const int cand = nb > per ? nb - sink - recent : 0;
     p.max_cand = std::max(p.max_cand, cand);
     sel_bytes += (double)cand * Hk * (2.0 * D + 4.0) + (k ? 8.0 * Hk * D : 0.0);
-    DecodeRow &r = dp.rows[i];
-    r.cache_row = qs[i].cache_row;
-    r.call_row = (uint16_t)(qs[i].tok - tok0);
-    r.pos = qs[i].pos;
-    r.nk = (n_sel - 1) * kSparseBlock + qs[i].slot % kSparseBlock + 1;
-    r.ctr = i;
-    kv_bytes += 4.0 * r.nk * Hk * D;
-    flops += 4.0 * r.nk * Hq * D;
   }
   cudaError_t e = timed(c, KV_KERNEL_SELECT, sel_bytes, 0, s,
                         [&] { return launch_select(p, s, c->pdl); });
@@ -2418,8 +2418,6 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
   dp.tmap_v = dp.tmap_v2 = c->tmV[layer];
   dp.tmap_k16 = c->tmK16[layer];
   dp.tmap_v16 = c->tmV16[layer];
-  dp.q = q + (int64_t)tok0 * Hq * D;
-  dp.out = out + (int64_t)tok0 * Hq * D;
   dp.q_row_stride = dp.out_row_stride = (int64_t)Hq * D;
   dp.rope = c->rope;
   dp.part_o = c->part_o;
@@ -2436,21 +2434,47 @@ int attend_selected(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_b
   dp.seg0_ring = 0;
   dp.ring_R = 1;
   dp.early_kv = 0;
-  dp.list = sp.list;
   dp.list_stride = sp.max_select;
   dp.scores = nullptr;
   dp.row_ml = nullptr;
   dp.list_sink = sink;
   dp.list_recent = recent;
-  static const int no_ring[kMaxRowsPerLaunch] = {};
-  // the partials are the cache's own: kMaxSplits slots for each of up to min(B, 512) rows
-  plan_decode_splits(c->num_sms, Hk, n, no_ring, dp,
-                     std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
-  for (int i = 0; i < n; ++i) dp.rows[i].split_tiles2 = qs[i].slot / kSparseBlock;
-  if (!c->pdl) dp.deep_pipeline = 0;
-  e = timed(c, KV_KERNEL_DECODE, kv_bytes + 4.0 * n * Hq * D, flops, s,
-            [&] { return launch_decode(dp, D, dp.rep <= 8 ? 1 : 2, s, c->pdl); });
-  return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+  // The attention in launches of about equally many queries (571 as 512 and 59: 86.4 us for the
+  // whole call, as 286 and 285: 79.2), whose tokens lie within 2^16 of the first one's (the
+  // kernel's 16-bit token index).
+  const int launches = (n + kMaxRowsPerLaunch - 1) / kMaxRowsPerLaunch;
+  const int most = (n + launches - 1) / launches;
+  for (int i0 = 0; i0 < n;) {
+    const int tok0 = qs[i0].tok;
+    double kv_bytes = 0, flops = 0;
+    int m = 0;
+    for (; i0 + m < n && m < most && qs[i0 + m].tok - tok0 <= 0xffff; ++m) {
+      const SparseQuery &w = qs[i0 + m];
+      const int n_sel = std::min(w.slot / kSparseBlock + 1, per);
+      DecodeRow &r = dp.rows[m];
+      r.cache_row = w.cache_row;
+      r.call_row = (uint16_t)(w.tok - tok0);
+      r.pos = w.pos;
+      r.nk = (n_sel - 1) * kSparseBlock + w.slot % kSparseBlock + 1;
+      r.ctr = m;
+      kv_bytes += 4.0 * r.nk * Hk * D;
+      flops += 4.0 * r.nk * Hq * D;
+    }
+    dp.q = q + (int64_t)tok0 * Hq * D;
+    dp.out = out + (int64_t)tok0 * Hq * D;
+    dp.list = sp.list + (int64_t)i0 * Hk * sp.max_select;
+    static const int no_ring[kMaxRowsPerLaunch] = {};
+    // the partials are the cache's own: kMaxSplits slots for each of up to min(B, 512) rows
+    plan_decode_splits(c->num_sms, Hk, m, no_ring, dp,
+                       std::min(c->B, kMaxRowsPerLaunch) * kMaxSplits);
+    for (int j = 0; j < m; ++j) dp.rows[j].split_tiles2 = qs[i0 + j].slot / kSparseBlock;
+    if (!c->pdl) dp.deep_pipeline = 0;
+    e = timed(c, KV_KERNEL_DECODE, kv_bytes + 4.0 * m * Hq * D, flops, s,
+              [&] { return launch_decode(dp, D, dp.rep <= 8 ? 1 : 2, s, c->pdl); });
+    if (e != cudaSuccess) return KV_ERR_CUDA;
+    i0 += m;
+  }
+  return KV_OK;
 }
 
 }  // namespace
@@ -2477,11 +2501,12 @@ int kv_sparse_enable(kv_cache *c, int max_select) try {
     sp.scale.push_back((float *)f);
     sp.valid.push_back(std::vector<int32_t>(c->kind[l] == KV_GLOBAL ? c->B : 0, 0));
   }
-  const size_t queries = (size_t)kMaxRowsPerLaunch * c->Hk;
-  ok = ok && cudaMalloc((void **)&sp.list, queries * max_select * 4) == cudaSuccess;
-  ok = ok && cudaMalloc((void **)&sp.counters, queries * 4) == cudaSuccess;
+  const size_t lists = (size_t)kMaxSelectQueries * c->Hk * max_select * 4;
+  const size_t tickets = (size_t)kMaxRowsPerLaunch * c->Hk * 4;
+  ok = ok && cudaMalloc((void **)&sp.list, lists) == cudaSuccess;
+  ok = ok && cudaMalloc((void **)&sp.counters, tickets) == cudaSuccess;
   const bool have = ok;
-  ok = ok && cudaMemset(sp.counters, 0, queries * 4) == cudaSuccess &&
+  ok = ok && cudaMemset(sp.counters, 0, tickets) == cudaSuccess &&
        cudaDeviceSynchronize() == cudaSuccess;
   if (!ok) {
     for (int8_t *p : sp.bound) cudaFree(p);
@@ -2578,14 +2603,14 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
     rc = update_bounds(c, layer, live, slots, kept, s);
     if (rc != KV_OK) return rc;
   }
-  // queries in launches of at most kMaxRowsPerLaunch, all about equally many (571 queries as
-  // 512 and 59: 86.4 us for the call, as 286 and 285: 79.2), whose tokens lie within 2^16 of the
-  // first one's (the kernels' 16-bit token index)
+  // the selections in launches of about equally many queries, of at most 512 rows
   int64_t total = 0;
   for (int i = 0; i < Bs; ++i) total += n_new[i];
-  const int64_t launches = (total + kMaxRowsPerLaunch - 1) / kMaxRowsPerLaunch;
+  const int cap = fused ? kMaxRowsPerLaunch : kMaxSelectQueries;
+  const int64_t launches = (total + cap - 1) / cap;
   const int64_t most = (total + launches - 1) / launches;
-  std::vector<SelectQuery> batch;
+  std::vector<SparseQuery> batch;
+  int batch_rows = 0;
   const auto flush = [&]() -> int {
     return attend_selected(c, layer, (const __nv_bfloat16 *)q, fused ? kb : nullptr,
                            fused ? vb : nullptr, (__nv_bfloat16 *)out, batch, sink, top_k, recent,
@@ -2594,12 +2619,14 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
   for (int i = 0; i < Bs; ++i)
     for (int t = 0; t < n_new[i]; ++t) {
       const int r = cache_rows[i], slot = slots_of(c, r) + t, tok = i * C + t;
-      if (!batch.empty() &&
-          ((int64_t)batch.size() == most || tok - batch[0].tok > 0xffff)) {
+      const bool next_row = batch.empty() || batch.back().cache_row != r;
+      if ((int64_t)batch.size() == most || (next_row && batch_rows == kMaxRowsPerLaunch)) {
         if ((rc = flush()) != KV_OK) return rc;
         batch.clear();
+        batch_rows = 0;
       }
-      SelectQuery sq = {r, slot, c->lens[r] + t, tok, 0, 0};
+      batch_rows += batch.empty() || batch.back().cache_row != r;
+      SparseQuery sq = {r, slot, c->lens[r] + t, tok, 0, 0};
       if (fused) {  // blocks complete with this token; known from now on up to the cached ones
         sq.pend0 = slot / kSparseBlock - valid[r] > 1 ? slot / kSparseBlock : valid[r];
         sq.n_pend = std::max(0, (slot + 1) / kSparseBlock - sq.pend0);

@@ -173,14 +173,26 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : D == 64 ? 5 : 4)
   __shared__ int warp_n[kSelWarps][2];
   __shared__ int pick[3];  // the digit that holds the threshold, keys above it and in it
 
-  const SelectQuery &qu = p.queries[blockIdx.x];
+  int r = blockIdx.x;  // the query's row: single tokens, a row each
+  if (!APPEND) {
+    int hi = p.n_rows - 1;
+    r = 0;
+    while (r < hi) {
+      const int mid = (r + hi + 1) >> 1;
+      if (p.rows[mid].q0 <= (int)blockIdx.x) r = mid;
+      else hi = mid - 1;
+    }
+  }
+  const SelectRow &row = p.rows[r];
+  const int nth = APPEND ? 0 : (int)blockIdx.x - row.q0;
+  const int slot = row.slot + nth, pos = row.pos + nth, tok = row.tok + nth;
   const int g = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nb = qu.slot / kSparseBlock + 1;
+  const int nb = slot / kSparseBlock + 1;
   const int per = p.sink + p.top_k + p.recent;
   const int n_sel = min(nb, per);
   const int n_cand = nb > per ? nb - p.sink - p.recent : 0;
   int32_t *list = p.list + ((int64_t)blockIdx.x * p.Hk + g) * p.list_stride;
-  int32_t *user = p.selected ? p.selected + ((int64_t)qu.tok * p.Hk + g) * per : nullptr;
+  int32_t *user = p.selected ? p.selected + ((int64_t)tok * p.Hk + g) * per : nullptr;
 
   // APPEND: q, k and v may come from the kernel before; else an append of this call lies
   // between, and whatever ran before that append has completed.
@@ -189,15 +201,15 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : D == 64 ? 5 : 4)
     // one row of 2k keys, 58.3 -> 57.9 for 64 of 1k-8k).  The same for the first one, two or
     // four blocks chosen below lost (60.6, 61.5, 62.9): the known blocks fill that time.
     if (tid == 0 && n_cand > 0)
-      ptx::prefetch_l2(p.bound + (((int64_t)qu.cache_row * p.Hk + g) * p.nb_cap + p.sink) * 2 * D,
+      ptx::prefetch_l2(p.bound + (((int64_t)row.cache_row * p.Hk + g) * p.nb_cap + p.sink) * 2 * D,
                        (uint32_t)n_cand * 2 * D);
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
   }
-  const float2 *cs = p.rope + (int64_t)qu.pos * kHalf;
+  const float2 *cs = p.rope + (int64_t)pos * kHalf;
   if (APPEND && warp == kSelWarps - 1) {  // the new key and value, 8 pairs per lane
-    const int64_t dst = kv_row(p.pt, qu.cache_row, p.Hk, g, p.seg_rows, qu.slot) * D;
-    const int64_t src = ((int64_t)qu.tok * p.Hk + g) * D;
+    const int64_t dst = kv_row(p.pt, row.cache_row, p.Hk, g, p.seg_rows, slot) * D;
+    const int64_t src = ((int64_t)tok * p.Hk + g) * D;
     if (lane < kHalf / 8) {
       const uint4 k1 = *reinterpret_cast<const uint4 *>(p.k + src + 8 * lane);
       const uint4 k2 = *reinterpret_cast<const uint4 *>(p.k + src + kHalf + 8 * lane);
@@ -225,7 +237,7 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : D == 64 ? 5 : 4)
     // The group's query heads, one warp each: rotate (float products without contraction,
     // one rounding to bf16, as the attention does), find the largest magnitude, quantise.
     for (int h = warp; h < p.rep; h += kSelWarps) {
-      const __nv_bfloat16 *q = p.q + ((int64_t)qu.tok * p.Hq + g * p.rep + h) * D;
+      const __nv_bfloat16 *q = p.q + ((int64_t)tok * p.Hq + g * p.rep + h) * D;
       float a[kHalf / 32], b[kHalf / 32], m = 0.f;
 #pragma unroll
       for (int i = 0; i < kHalf / 32; ++i) {
@@ -272,9 +284,9 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : D == 64 ? 5 : 4)
         user[i] = nb - per + i;
   }
   __syncthreads();  // q8 and, APPEND, the stored key
-  if (APPEND && qu.n_pend > 0) {
-    for (int i = warp; i < qu.n_pend; i += kSelWarps)
-      bounds_of_block<D>(p.cache_k, p.pt, p.seg_rows, qu.cache_row, p.Hk, g, qu.pend0 + i,
+  if (APPEND && row.n_pend > 0) {
+    for (int i = warp; i < row.n_pend; i += kSelWarps)
+      bounds_of_block<D>(p.cache_k, p.pt, p.seg_rows, row.cache_row, p.Hk, g, row.pend0 + i,
                          p.nb_cap, p.bound, p.scale, lane);
     __syncthreads();
   }
@@ -286,9 +298,9 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : D == 64 ? 5 : 4)
   {
     constexpr int kWords = D / 32;  // 4-byte words per lane
     const int sub = tid & 7;
-    const int8_t *bound = p.bound + ((int64_t)qu.cache_row * p.Hk + g) * p.nb_cap * 2 * D +
+    const int8_t *bound = p.bound + ((int64_t)row.cache_row * p.Hk + g) * p.nb_cap * 2 * D +
                           4 * kWords * sub;
-    const float *scale = p.scale + ((int64_t)qu.cache_row * p.Hk + g) * p.nb_cap;
+    const float *scale = p.scale + ((int64_t)row.cache_row * p.Hk + g) * p.nb_cap;
     // a warp takes 16 blocks per pass, all of its lanes as many passes (the shuffles below)
     for (int c0 = 16 * warp; c0 < n_cand; c0 += kSelThreads / 2) {
       const int cg = c0 + 4 * (lane / 8);

@@ -104,6 +104,20 @@ def test_more_queries_than_a_launch_holds():
 
 
 @pytest.mark.gpu
+def test_more_queries_than_a_selection_holds():
+    """1100 tokens, a row's chunk between two selections; 600 rows, of one or two tokens."""
+    r = Rows(9, 700, 2, 1, 64, [0, 400, 3, 64, 200, 17, 0, 99, 1], seed=14)
+    r.cache.enable_sparse(4)
+    step(r, [130, 61, 130, 130, 130, 130, 130, 129, 130], 1, 1, 1)
+    step(r, [1] * 9, 1, 2, 1)
+    lens = [(37 * i) % 290 for i in range(600)]
+    r = Rows(600, 300, 2, 1, 64, lens, seed=15)
+    r.cache.enable_sparse(3)
+    step(r, [1 + (i % 3 == 1) for i in range(600)], 0, 1, 1)
+    step(r, [1] * 600, 1, 1, 1)
+
+
+@pytest.mark.gpu
 def test_far_apart_queries_of_one_call():
     """Token indices more than 2^16 apart in q."""
     import torch
