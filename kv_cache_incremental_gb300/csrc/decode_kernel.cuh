@@ -596,9 +596,9 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
   float *scores = nullptr;  // of the row's query heads of this kv head
   if (SCORES && p.scores)
     scores = p.scores + ((int64_t)row_idx * p.Hq + g * p.rep) * p.score_stride;
+  int s = 0, phase = 0;  // the tile's stage, and its use of it modulo 2
   for (int it = 0; it < n_tiles; ++it) {
-    const int s = it % kStages;
-    if (*fail || !ptx::mbar_wait(&full[s], (it / kStages) & 1, kWaitLimit)) {
+    if (*fail || !ptx::mbar_wait(&full[s], phase, kWaitLimit)) {
       atomicExch(p.err, 1);
       *fail = 1;
       break;
@@ -627,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : D == 128 ? 2 : MODE == kD
                                   scores ? scores + key_base : nullptr, p.score_stride, p.rep);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&empty[s]);
+    if (++s == kStages) s = 0, phase ^= 1;
   }
   if (owner && warp == 0 && !*fail)  // the new key, from the mini-tile (row 0 only)
     attend16<D, NT, SCORES, LAZY>(acc, qb, mini_k, mini_v, kMiniRows * 128, 0, 1, -1,
