@@ -2610,6 +2610,7 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
   const int64_t launches = (total + cap - 1) / cap;
   const int64_t most = (total + launches - 1) / launches;
   std::vector<SparseQuery> batch;
+  batch.reserve((size_t)most);  // no host memory is asked for once `valid` has been raised
   int batch_rows = 0;
   const auto flush = [&]() -> int {
     return attend_selected(c, layer, (const __nv_bfloat16 *)q, fused ? kb : nullptr,
