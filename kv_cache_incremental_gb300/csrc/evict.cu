@@ -28,13 +28,13 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// HELD: the row's weights stay in shared memory (every launch whose rows fit).
 // The number order_key makes, back to its weight (a NaN to the plain one, -0 to +0).
 __device__ __forceinline__ float key_weight(uint32_t k) {
   if (k == 0) return __int_as_float(0x7FC00000);
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
+// HELD: the row's weights stay in shared memory (every launch whose rows fit).
 template <bool HELD>
 __global__ void __launch_bounds__(kThreads)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
@@ -71,6 +71,9 @@ __global__ void __launch_bounds__(kThreads)
         if (cut && i < n) atomicAdd(&hist[k >> 21], 1);
       }
     }
+    // Whatever follows reads keys that other threads stored -- also when nothing competes
+    // (recent == keep, or a row that keeps everything) -- and may write acc_out over acc_in.
+    __syncthreads();
   }
   const auto key_at = [&](int i) { return HELD ? held[i] : order_key(acc[i]); };
   uint32_t prefix = 0;  // keys above it are kept, and the first `ties` at it
@@ -85,13 +88,14 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
         __syncthreads();
       }
-      if (!HELD || pass > 0)
+      if (!HELD || pass > 0) {  // HELD: the first digit's was made with the load
 #pragma unroll 4
         for (int i = tid; i < n; i += kThreads) {
           const uint32_t k = key_at(i);
           if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1);
         }
-      __syncthreads();
+        __syncthreads();
+      }
       // Bins from the largest down, two per thread; each warp scans its 64, then adds the
       // totals of the warps before it.
       const int top = kBins - 1 - 2 * tid;
