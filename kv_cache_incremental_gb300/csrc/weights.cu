@@ -32,6 +32,7 @@ constexpr int kWarps = 8, kWThreads = kWarps * 32;
 // one and two eights for single tokens ran no faster (8 counted vectors, 24 rows of 6k keys:
 // 54.7 us with eight, 54.9 with one).
 constexpr int QT = 8;
+constexpr int kEights = 2;  // eights of vectors that a step takes together
 static_assert(kWeightTile == kWarps * 16, "one 16-key fragment per warp");
 
 __device__ __forceinline__ int find_weights_row(const WeightsParams &p, int item) {
@@ -50,43 +51,44 @@ template <int D>
 constexpr int kQStride = 2 * D + 64;
 
 // Query vectors [v0, v0 + 8 QT) of the row, rotated and rounded to bf16 as the attention
-// rotates them, into shared memory, with their -m and 1 / l and the last slot that each sees;
-// vectors past the last are zero, see nothing and weigh 2^(0 - inf) * 0.
+// rotates them, into shared memory, with their -m and 1 / l and the last slot that each sees.
+// sum_step takes them by kEights eights; the vectors that fill up the last of these are copies of
+// the row's last one with a 1 / l of 0.  They add 0 wherever that one's weight is a number (zeros
+// in their place made NaN of 0 * inf at keys with infinite components that nothing weighs).
 template <int D>
 __device__ __forceinline__ void load_queries(const WeightsParams &p, const WeightsRow &row, int g,
                                              int v0, int n_vec, uint8_t *qs, float2 *ml,
                                              int *limit) {
-  constexpr int kHalf = D / 2, kVec = kHalf / 8;
-  if (threadIdx.x < 8 * QT) {
-    const int vec = v0 + threadIdx.x;
+  constexpr int kHalf = D / 2, kVec = kHalf / 8, kFill = 8 * kEights;
+  const int taken = min(8 * QT, (n_vec - v0 + kFill - 1) / kFill * kFill);
+  if (threadIdx.x < taken) {
+    const int vec = min(v0 + (int)threadIdx.x, n_vec - 1);
+    const bool fill = v0 + (int)threadIdx.x >= n_vec;
     const int t = row.t0 + vec / p.rep;
-    float2 e = make_float2(INFINITY, 0.f);
-    if (vec < n_vec)
-      e = p.ml[((int64_t)row.call_row * kChunk + t - row.tok0) * p.Hq + g * p.rep + vec % p.rep];
-    ml[threadIdx.x] = make_float2(-e.x, e.y);
-    limit[threadIdx.x] = vec < n_vec ? row.slots + t : -1;
+    const float2 e =
+        p.ml[((int64_t)row.call_row * kChunk + t - row.tok0) * p.Hq + g * p.rep + vec % p.rep];
+    ml[threadIdx.x] = make_float2(-e.x, fill ? 0.f : e.y);
+    limit[threadIdx.x] = fill ? -1 : row.slots + t;
   }
-  for (int u = threadIdx.x; u < 8 * QT * kVec; u += kWThreads) {
-    const int i = u / kVec, c = u % kVec, vec = v0 + i;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (vec < n_vec) {
-      const int t = row.t0 + vec / p.rep, h = vec % p.rep;
-      const __nv_bfloat16 *q = p.q + (int64_t)row.call_row * p.q_row_stride +
-                               ((int64_t)t * p.Hq + g * p.rep + h) * D;
-      const uint4 x1v = *reinterpret_cast<const uint4 *>(q + 8 * c);
-      const uint4 x2v = *reinterpret_cast<const uint4 *>(q + kHalf + 8 * c);
-      const __nv_bfloat16 *x1 = reinterpret_cast<const __nv_bfloat16 *>(&x1v);
-      const __nv_bfloat16 *x2 = reinterpret_cast<const __nv_bfloat16 *>(&x2v);
-      __nv_bfloat16 *o1 = reinterpret_cast<__nv_bfloat16 *>(&lo);
-      __nv_bfloat16 *o2 = reinterpret_cast<__nv_bfloat16 *>(&hi);
-      const float2 *cs = p.rope + (int64_t)(row.slots + row.shift + t) * kHalf + 8 * c;
+  for (int u = threadIdx.x; u < taken * kVec; u += kWThreads) {
+    const int i = u / kVec, c = u % kVec, vec = min(v0 + i, n_vec - 1);
+    const int t = row.t0 + vec / p.rep, h = vec % p.rep;
+    const __nv_bfloat16 *q = p.q + (int64_t)row.call_row * p.q_row_stride +
+                             ((int64_t)t * p.Hq + g * p.rep + h) * D;
+    const uint4 x1v = *reinterpret_cast<const uint4 *>(q + 8 * c);
+    const uint4 x2v = *reinterpret_cast<const uint4 *>(q + kHalf + 8 * c);
+    const __nv_bfloat16 *x1 = reinterpret_cast<const __nv_bfloat16 *>(&x1v);
+    const __nv_bfloat16 *x2 = reinterpret_cast<const __nv_bfloat16 *>(&x2v);
+    uint4 lo, hi;
+    __nv_bfloat16 *o1 = reinterpret_cast<__nv_bfloat16 *>(&lo);
+    __nv_bfloat16 *o2 = reinterpret_cast<__nv_bfloat16 *>(&hi);
+    const float2 *cs = p.rope + (int64_t)(row.slots + row.shift + t) * kHalf + 8 * c;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = __bfloat162float(x1[j]), b = __bfloat162float(x2[j]);
-        const float2 e = cs[j];
-        o1[j] = __float2bfloat16_rn(__fsub_rn(__fmul_rn(a, e.x), __fmul_rn(b, e.y)));
-        o2[j] = __float2bfloat16_rn(__fadd_rn(__fmul_rn(a, e.y), __fmul_rn(b, e.x)));
-      }
+    for (int j = 0; j < 8; ++j) {
+      const float a = __bfloat162float(x1[j]), b = __bfloat162float(x2[j]);
+      const float2 e = cs[j];
+      o1[j] = __float2bfloat16_rn(__fsub_rn(__fmul_rn(a, e.x), __fmul_rn(b, e.y)));
+      o2[j] = __float2bfloat16_rn(__fadd_rn(__fmul_rn(a, e.y), __fmul_rn(b, e.x)));
     }
     *reinterpret_cast<uint4 *>(qs + i * kQStride<D> + 16 * c) = lo;
     *reinterpret_cast<uint4 *>(qs + i * kQStride<D> + D + 16 * c) = hi;
@@ -162,7 +164,8 @@ __device__ __forceinline__ void sum_step(const uint4 (&f)[D / 16], const uint8_t
                                          const int *limit, const float2 *ml,
                                          int n_nt, int key, float scale, int lane, float &sum0,
                                          float &sum1) {
-  constexpr int N = 2;
+  constexpr int N = kEights;
+  static_assert(QT % N == 0, "whole steps");
 #pragma unroll
   for (int nt0 = 0; nt0 < QT; nt0 += N) {
     if (nt0 >= n_nt) break;
