@@ -2610,12 +2610,16 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
   const int64_t launches = (total + cap - 1) / cap;
   const int64_t most = (total + launches - 1) / launches;
   std::vector<SparseQuery> batch;
-  batch.reserve((size_t)most);  // no host memory is asked for once `valid` has been raised
+  batch.reserve((size_t)most);
   int batch_rows = 0;
   const auto flush = [&]() -> int {
-    return attend_selected(c, layer, (const __nv_bfloat16 *)q, fused ? kb : nullptr,
-                           fused ? vb : nullptr, (__nv_bfloat16 *)out, batch, sink, top_k, recent,
-                           selected, s);
+    const int e = attend_selected(c, layer, (const __nv_bfloat16 *)q, fused ? kb : nullptr,
+                                  fused ? vb : nullptr, (__nv_bfloat16 *)out, batch, sink, top_k,
+                                  recent, selected, s);
+    if (e == KV_OK && fused && !capturing)  // the launch bounds each row's cached blocks
+      for (const SparseQuery &w : batch)
+        valid[w.cache_row] = std::max(valid[w.cache_row], w.slot / kSparseBlock);
+    return e;
   };
   for (int i = 0; i < Bs; ++i)
     for (int t = 0; t < n_new[i]; ++t) {
@@ -2628,10 +2632,9 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
       }
       batch_rows += batch.empty() || batch.back().cache_row != r;
       SparseQuery sq = {r, slot, c->lens[r] + t, tok, 0, 0};
-      if (fused) {  // blocks complete with this token; known from now on up to the cached ones
+      if (fused) {  // blocks complete with this token
         sq.pend0 = slot / kSparseBlock - valid[r] > 1 ? slot / kSparseBlock : valid[r];
         sq.n_pend = std::max(0, (slot + 1) / kSparseBlock - sq.pend0);
-        if (!capturing) valid[r] = std::max(valid[r], slot / kSparseBlock);
       }
       batch.push_back(sq);
     }
