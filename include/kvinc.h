@@ -106,12 +106,11 @@ enum kv_status {
  * and V, the RoPE table [max_len][D/2] of (cos, sin) float pairs computed on
  * the host in double, decode split-K partials (min(B, 512) x 32 x Hq vectors of
  * D floats) and chunked-prefill key-split partials (min(1024 x SMs,
- * B x Hq x 64 x 16) vectors of D floats, or, with a global layer, room for the scores of
- * kv_append_weights where that is more: B x Hq x max_len floats, at most 2048 x SMs
- * vectors; with a global layer also B x 64 x Hq pairs of floats).  Every later call works
+ * B x Hq x 64 x 16) vectors of D floats).  Every later call works
  * within this memory: none allocates device memory except kv_append_host / kv_append_hybrid_host
  * with pageable buffers (their staging), kv_step_graph_create (the graph's own
- * resources, at instantiation) and kv_sparse_enable.  All lens start at 0.
+ * resources, at instantiation), kv_sparse_enable and a cache's first kv_append_weights.
+ * All lens start at 0.
  * On success *out holds the cache; on failure *out is NULL.
  */
 int kv_cache_create(kv_cache **out, int B, int max_len, int Hq, int Hk, int D, int W,
@@ -520,7 +519,11 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
  *   Other entries of acc_out (rows without new tokens, slots j >= s + n) are not written, so
  *   nothing has to be cleared when a row starts over.  last >= 1; a prompt's chunk may count
  *   its last few queries only.  Sums are in float, in an order that does not vary between
- *   runs.  KV_ERR_ARG on other layer kinds.
+ *   runs.  KV_ERR_ARG on other layer kinds.  A cache's first call with new tokens allocates what
+ *   counting needs, kept until the cache is destroyed (also if that call is being captured into a
+ *   graph): B x 64 x Hq pairs of floats and, where the prefill partials are smaller, room for
+ *   scores of B x Hq x (max_len + 3) floats, at most 2048 x SMs vectors of D; KV_ERR_OOM if it
+ *   cannot be had, before anything is enqueued.
  *
  * kv_evict_rows: for i < n, destination row dst_rows[i] of `dst` becomes source row
  *   src_rows[i] of `src` with at most `keep` of its keys on every global layer: per layer and

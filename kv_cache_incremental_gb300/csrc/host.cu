@@ -137,9 +137,11 @@ struct kv_cache {
   float *ppart_o = nullptr;
   float2 *ppart_ml = nullptr;
   int64_t ppart_cap = 0;  // vectors
-  // accumulated weights: (m, 1 / l) of the query vectors of a sub-chunk, [B][kChunk][Hq]
-  // (caches with a global layer)
+  // accumulated weights (ensure_weights_room: from the first call on that counts): (m, 1 / l)
+  // of the query vectors of a sub-chunk, [B][kChunk][Hq], and room for the scores of decode
+  // rows -- the prefill partials where they are as large, else a buffer of its own
   float2 *ml = nullptr;
+  float *scores = nullptr, *own_scores = nullptr;
   // host-buffer entry point staging
   void *stage = nullptr;
   size_t stage_bytes = 0;
@@ -614,13 +616,39 @@ int64_t prefill_part_reserve(int num_sms, int B, int Hq) {
   return std::min<int64_t>(prefill_part_cap(num_sms),
                            (int64_t)B * Hq * kChunk * kMaxPrefillSplits);
 }
-// The same memory, in vectors of D floats, holds the scores of an accumulating decode call
-// (kv_append_weights): one float per row, query head and slot, up to twice the prefill bound.
-// With the prefill bound alone 16 rows of 16k-32k keys at Hq = 64 took two launches and 329
-// us, with this one launch and 294 us.
-int64_t score_reserve(int num_sms, int B, int Hq, int max_len, int D) {
-  return std::min<int64_t>(2 * prefill_part_cap(num_sms),
-                           ((int64_t)B * Hq * ((int64_t)max_len + 3) + D - 1) / D);
+// Floats of room for the scores of an accumulating decode call (kv_append_weights): one per
+// row, query head and slot, up to twice the prefill partials' bound, and no less than a cache's
+// prefill partials, which the scores then share.  With the prefill bound alone 16 rows of
+// 16k-32k keys at Hq = 64 took two launches and 329 us, with twice that one launch and 294 us.
+int64_t score_room(const kv_cache *c) {
+  const int64_t all = (int64_t)c->B * c->Hq * ((int64_t)c->max_len + 3);
+  return std::max(c->ppart_cap * c->D,
+                  std::min<int64_t>(2 * prefill_part_cap(c->num_sms) * c->D, all));
+}
+
+// The memory of accumulated weights, on the cache's first call that counts them: caches that
+// never do hold none of it.  Nothing is enqueued, and a capture in progress on this thread or
+// another goes on (the memory belongs to the cache, not to the graph).
+int ensure_weights_room(kv_cache *c) {
+  if (c->ml) return KV_OK;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return KV_ERR_CUDA;
+  const int64_t room = score_room(c);
+  float *own = nullptr;
+  float2 *ml = nullptr;
+  bool ok = cudaMalloc((void **)&ml, (size_t)c->B * kChunk * c->Hq * sizeof(float2)) == cudaSuccess;
+  if (ok && room > c->ppart_cap * c->D)
+    ok = cudaMalloc((void **)&own, (size_t)room * sizeof(float)) == cudaSuccess;
+  if (!ok) {
+    cudaGetLastError();
+    cudaFree(ml);
+  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (!ok) return KV_ERR_OOM;
+  c->ml = ml;
+  c->own_scores = own;
+  c->scores = own ? own : c->ppart_o;
+  return KV_OK;
 }
 
 // The prefill entries of one sub-chunk, per launch kind, with their key splits; the
@@ -997,6 +1025,7 @@ void free_all(kv_cache *c) {
   cudaFree(c->ppart_o);
   cudaFree(c->ppart_ml);
   cudaFree(c->ml);
+  cudaFree(c->own_scores);
   cudaFree(c->stage);
   cudaFree(c->table);
   for (int8_t *p : c->sparse.bound) cudaFree(p);
@@ -1188,15 +1217,9 @@ static int create_impl(kv_cache **out, int B, int max_len, int Hq, int Hk, int D
   // prefill key-split partials: every call's plan fits (plan_prefill), so kv_append never
   // allocates
   c->ppart_cap = prefill_part_reserve(c->num_sms, B, Hq);
-  for (int k : c->kind)
-    if (k == KV_GLOBAL)
-      c->ppart_cap = std::max(c->ppart_cap, score_reserve(c->num_sms, B, Hq, max_len, D));
   if (!alloc((void **)&c->ppart_o, (size_t)c->ppart_cap * D * 4) ||
       !alloc((void **)&c->ppart_ml, (size_t)c->ppart_cap * 8))
     return fail(KV_ERR_OOM);
-  for (int k : c->kind)
-    if (k == KV_GLOBAL && !c->ml && !alloc((void **)&c->ml, (size_t)B * kChunk * Hq * 8))
-      return fail(KV_ERR_OOM);
   if (cudaDeviceSynchronize() != cudaSuccess) return fail(KV_ERR_CUDA);
   if (const char *pdl = std::getenv("KVINC_PDL")) c->pdl = pdl[0] != '0';
   if (const char *log = std::getenv("KVINC_LOG")) {
@@ -2654,7 +2677,7 @@ struct SingleIn {
 };
 
 // Append, attention and weights of single-token rows.  With `store` in one pass over their
-// keys: decode launches that store the scores in the prefill partials' reserve, each followed
+// keys: decode launches that store the scores in the room for them, each followed
 // by the join; a launch takes as many rows as fit there together, all launches about equally
 // many.  Without, for rows whose scores alone are too many, the weights take a pass over K.
 int decode_counted(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
@@ -2666,7 +2689,7 @@ int decode_counted(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bf
   int longest = 0;
   for (const SingleIn &w : in) longest = std::max(longest, slots_of(c, w.cache_row) + 1);
   const int64_t stride = (longest + 3) / 4 * 4;
-  const int64_t room = store ? c->ppart_cap * c->D / (c->Hq * stride) : kMaxRowsPerLaunch;
+  const int64_t room = store ? score_room(c) / (c->Hq * stride) : kMaxRowsPerLaunch;
   const size_t most = (size_t)std::min<int64_t>(room, kMaxRowsPerLaunch);
   const size_t launches = (in.size() + most - 1) / most;
   const size_t per = (in.size() + launches - 1) / launches;
@@ -2690,7 +2713,7 @@ int decode_counted(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bf
     double bytes = 0, fl = 0;
     fill_decode(c, layer, q, k, v, out, (int64_t)C * c->Hq * c->D, (int64_t)C * c->Hk * c->D,
                 batch, dp, bytes, fl);
-    dp.scores = store ? c->ppart_o : nullptr;
+    dp.scores = store ? c->scores : nullptr;
     dp.row_ml = c->ml;
     dp.score_stride = stride;
     dp.early_kv = early_kv_ok(c, layer, s) ? 1 : 0;
@@ -2704,7 +2727,7 @@ int decode_counted(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bf
       if (rc != KV_OK) return rc;
       continue;
     }
-    jp.scores = c->ppart_o;
+    jp.scores = c->scores;
     jp.row_ml = c->ml;
     jp.score_stride = stride;
     jp.acc_in = cnt.acc_in;
@@ -2732,7 +2755,7 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
   std::vector<int32_t> cache_rows;
   int rc = check_rows(c, n_new, rows, Bs, C, cache_rows);
   if (rc != KV_OK) return rc;
-  // Single-token rows apart: in one pass over their keys while a row's scores fit the reserve.
+  // Single-token rows apart: in one pass over their keys while a row's scores fit the room.
   std::vector<SingleIn> stored, longer;
   std::vector<int32_t> n_rest(n_new, n_new + std::max(Bs, 0)), t0(std::max(Bs, 0), 0);
   std::vector<std::pair<int, int>> want;
@@ -2747,7 +2770,7 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
       continue;
     }
     const int64_t stride = (slots + 1 + 3) / 4 * 4;
-    (stride * Hq <= c->ppart_cap * c->D ? stored : longer).push_back({cache_rows[i], i});
+    (stride * Hq <= score_room(c) ? stored : longer).push_back({cache_rows[i], i});
     n_rest[i] = 0;
   }
   if (want.empty()) return KV_OK;
@@ -2757,6 +2780,8 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
     return KV_ERR_ARG;
   DeviceGuard guard(c->device);
   cudaStream_t s = (cudaStream_t)stream;
+  rc = ensure_weights_room(c);
+  if (rc != KV_OK) return rc;
   rc = ensure_blocks(c, want, s);  // every row's, before anything else is enqueued
   if (rc != KV_OK) return rc;
   c->cur_layer = layer;

@@ -49,7 +49,7 @@ class Cache:
         self.lib.kv_cache_destroy(self.h)
 
     def append(self, n_new, rows=None, layer=0, C=None):
-        return self.lib.kv_append(self.h, layer, PTR, PTR, PTR, self.Hq, C or max(n_new),
+        return self.lib.kv_append(self.h, layer, PTR, PTR, PTR, self.Hq, C or max(1, *n_new),
                                   i32(n_new), i32(rows), len(n_new), PTR, None)
 
     def advance(self, n_new, rows=None):
@@ -62,12 +62,12 @@ class Cache:
                                               self.lib.kv_export_bytes(self.h, n), None) == 0
 
     def sparse(self, n_new, top_k, sink=1, recent=2, rows=None, layer=0, selected=None):
-        return self.lib.kv_append_sparse(self.h, layer, PTR, PTR, PTR, self.Hq, max(n_new),
+        return self.lib.kv_append_sparse(self.h, layer, PTR, PTR, PTR, self.Hq, max(1, *n_new),
                                          i32(n_new), i32(rows), len(n_new), sink, top_k, recent,
                                          PTR, selected, None)
 
     def weights(self, n_new, acc_in=PTR, acc_out=PTR, last=1, rows=None, layer=0):
-        return self.lib.kv_append_weights(self.h, layer, PTR, PTR, PTR, self.Hq, max(n_new),
+        return self.lib.kv_append_weights(self.h, layer, PTR, PTR, PTR, self.Hq, max(1, *n_new),
                                           i32(n_new), i32(rows), len(n_new), last, acc_in,
                                           acc_out, PTR, None)
 

@@ -61,3 +61,61 @@ def test_bounds_of_a_sparse_step_that_ran_are_known(lib):
     assert lib.kv_sparse_update(c.h, 0, None, 2, None) == 0
     assert names(c) == ["bounds_kernel"]
     c.close()
+
+
+def created_bytes(B, max_len, Hq, Hk, D, layers, sms=152):
+    """Device memory of a dense cache of global layers, as kv_cache_create documents it."""
+    kv = layers * 2 * B * Hk * (max_len + 1) * D * 2
+    scratch = 2 * B * Hk * 64 * D * 2
+    rope = max_len * (D // 2) * 8
+    partials = (min(B, 512) * 32 * Hq + min(1024 * sms, B * Hq * 64 * 16)) * (D * 4 + 8)
+    return kv + scratch + rope + partials + B * Hk * 4 + 16     # tickets, error word
+
+
+@pytest.mark.parametrize("B,max_len,Hq,Hk,D,layers", [
+    (16, 32768, 64, 8, 128, 6), (64, 8192, 32, 8, 128, 1), (1, 512, 8, 2, 64, 1),
+    (3, 1 << 20, 64, 4, 64, 1)])
+def test_memory_of_a_cache_that_counts_no_weights(lib, B, max_len, Hq, Hk, D, layers):
+    """The memory of accumulated weights is allocated by a cache's first call that counts them,
+    once, and by no other call."""
+    c = Cache(lib, B, max_len, Hq, Hk, D, kinds=(0,) * layers)
+    assert lib.fake_live_bytes() == created_bytes(B, max_len, Hq, Hk, D, layers)
+    c.fill([min(300, max_len - 40)] * B)
+    before = lib.fake_live_bytes()
+    assert c.append([1] * B) == 0 and c.append([30] * B) == 0
+    assert c.weights([0] * B) == 0 and lib.fake_live_bytes() == before
+    assert c.weights([1] * B) == 0
+    scores = min(B * Hq * (max_len + 3), 2 * 1024 * 152 * D)
+    if scores <= min(1024 * 152, B * Hq * 64 * 16) * D:
+        scores = 0                                     # the prefill partials hold them
+    assert lib.fake_live_bytes() == before + B * 64 * Hq * 8 + 4 * scores
+    after = lib.fake_live_bytes()
+    assert c.weights([1] * B) == 0 and c.weights([30] * B, last=9) == 0
+    assert lib.fake_live_bytes() == after
+    c.close()
+    assert lib.fake_live_blocks() == 0
+    lib.fake_reset()
+
+
+def test_a_first_counting_call_without_memory_changes_nothing(lib):
+    for nth in range(2):                               # either of its two allocations
+        c = Cache(lib, 2, 100000, 8, 2, 64, blocks=4000)
+        c.fill([100, 50])
+        was, held = c.state(), lib.fake_live_bytes()
+        names(c)
+        lib.fake_fail_malloc(nth)
+        assert c.weights([1, 20]) == 5                 # KV_ERR_OOM
+        assert names(c) == [] and c.state() == was and lib.fake_live_bytes() == held
+        assert c.weights([1, 20]) == 0
+        c.close()
+        lib.fake_reset()
+
+
+def test_a_first_counting_call_may_be_captured(lib):
+    c = Cache(lib, 2, 30000, 8, 2, 64)
+    c.fill([100, 50])
+    lib.fake_capturing(1)
+    assert c.weights([1, 20]) == 0
+    assert lib.fake_bad_mallocs() == 0                 # none under a mode that refuses them
+    lib.fake_reset()
+    c.close()
