@@ -454,6 +454,15 @@ int kvinc::plan_decode_splits(int num_sms, int Hk, int n, const int *nk2, Decode
 
 namespace {
 
+// End of the decode launch that starts at in[r0], rows in the order of the call: at most `most`
+// rows, whose call rows lie within 2^16 of the first one's (DecodeRow's 16-bit index).
+template <class Row>
+size_t batch_end(const std::vector<Row> &in, size_t r0, size_t most) {
+  size_t r1 = std::min(in.size(), r0 + most);
+  while (in[r1 - 1].call_row - in[r0].call_row > 0xffff) --r1;
+  return r1;
+}
+
 // Split-K schedule for one batch of decode rows (<= kMaxRowsPerLaunch).  Segment 0 holds
 // storage slots [0, nk) of the layer storage (the ring of a sliding layer, else a cache);
 // a hybrid layer adds segment 1, its own ring, with its own splits.  Merge tickets are
@@ -467,7 +476,7 @@ void plan_decode(const Geom &g, const std::vector<DecodeIn> &in, DecodeParams &p
   for (size_t i = 0; i < in.size(); ++i) {
     DecodeRow &r = p.rows[i];
     r.cache_row = in[i].cache_row;
-    r.call_row = (uint16_t)in[i].call_row;
+    r.call_row = (uint16_t)(in[i].call_row - in[0].call_row);  // batch_end
     r.pos = in[i].pos;
     r.nk = sliding ? std::min(in[i].pos + 1, g.R) : in[i].slot + 1;
     r.ctr = in[i].cache_row;
@@ -485,26 +494,29 @@ void plan_decode(const Geom &g, const std::vector<DecodeIn> &in, DecodeParams &p
 // batch of single-token rows; kv_bytes and flops are the algorithmic counts.
 // A hybrid layer's segment 0 is its group's cache: its new global key (k, v) is appended
 // by the kernel on a full layer only (on a local layer that key is already in the cache);
-// segment 1 is its ring, which takes the new local key (k_local, v_local).
+// segment 1 is its ring, which takes the new local key (k_local, v_local).  The launch's
+// pointers into the call's tensors are those of the batch's first call row.
 void fill_decode(const kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
                  const __nv_bfloat16 *v, __nv_bfloat16 *out, int64_t q_row, int64_t kv_row,
                  const std::vector<DecodeIn> &batch, DecodeParams &dp, double &bytes,
                  double &flops, const __nv_bfloat16 *k_local = nullptr,
                  const __nv_bfloat16 *v_local = nullptr) {
   const bool hybrid = is_hybrid(c->kind[layer]);
+  const int64_t call0 = batch[0].call_row;
+  const auto of_row0 = [&](const __nv_bfloat16 *p) { return p ? p + call0 * kv_row : p; };
   dp.tmap_k = c->tmK[layer];
   dp.tmap_v = c->tmV[layer];
-  dp.q = q;
+  dp.q = q + call0 * q_row;
   dp.q_row_stride = q_row;
-  dp.out = out;
+  dp.out = out + call0 * q_row;
   dp.out_row_stride = q_row;
   dp.rope = c->rope;
   dp.part_o = c->part_o;
   dp.part_ml = c->part_ml;
   dp.counters = c->counters;
   dp.err = c->err;
-  dp.k_new = k;
-  dp.v_new = v;
+  dp.k_new = of_row0(k);
+  dp.v_new = of_row0(v);
   dp.kv_row_stride = kv_row;
   dp.cache_k = (__nv_bfloat16 *)c->K[layer];
   dp.cache_v = (__nv_bfloat16 *)c->V[layer];
@@ -524,8 +536,8 @@ void fill_decode(const kv_cache *c, int layer, const __nv_bfloat16 *q, const __n
   dp.row_ml = nullptr;
   dp.tmap_k2 = hybrid ? c->tmRK[layer] : c->tmK[layer];
   dp.tmap_v2 = hybrid ? c->tmRV[layer] : c->tmV[layer];
-  dp.k_new2 = k_local;
-  dp.v_new2 = v_local;
+  dp.k_new2 = of_row0(k_local);
+  dp.v_new2 = of_row0(v_local);
   dp.cache_k2 = (__nv_bfloat16 *)c->RK[layer];
   dp.cache_v2 = (__nv_bfloat16 *)c->RV[layer];
   dp.seg_rows2 = c->R + 1;
@@ -829,8 +841,8 @@ int append_device(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bfl
     }
 
     // ---- split-K decode for single-token rows (append and split merge fused in)
-    for (size_t r0 = 0; r0 < drows.size(); r0 += kMaxRowsPerLaunch) {
-      const size_t r1 = std::min(drows.size(), r0 + kMaxRowsPerLaunch);
+    for (size_t r0 = 0, r1; r0 < drows.size(); r0 = r1) {
+      r1 = batch_end(drows, r0, kMaxRowsPerLaunch);
       std::vector<DecodeIn> batch(drows.begin() + r0, drows.begin() + r1);
       double bytes = 0, fl = 0;
       fill_decode(c, layer, q, k, v, out, q_row, kv_row, batch, dp, bytes, fl, kl, vl);
@@ -2693,8 +2705,8 @@ int decode_counted(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bf
   const size_t most = (size_t)std::min<int64_t>(room, kMaxRowsPerLaunch);
   const size_t launches = (in.size() + most - 1) / most;
   const size_t per = (in.size() + launches - 1) / launches;
-  for (size_t r0 = 0; r0 < in.size(); r0 += per) {
-    const size_t r1 = std::min(in.size(), r0 + per);
+  for (size_t r0 = 0, r1; r0 < in.size(); r0 = r1) {
+    r1 = batch_end(in, r0, per);
     std::vector<DecodeIn> batch;
     std::vector<WeightsRow> pass;
     jp.n_items = 0;
@@ -2714,7 +2726,7 @@ int decode_counted(kv_cache *c, int layer, const __nv_bfloat16 *q, const __nv_bf
     fill_decode(c, layer, q, k, v, out, (int64_t)C * c->Hq * c->D, (int64_t)C * c->Hk * c->D,
                 batch, dp, bytes, fl);
     dp.scores = store ? c->scores : nullptr;
-    dp.row_ml = c->ml;
+    dp.row_ml = c->ml + (int64_t)in[r0].call_row * kChunk * c->Hq;
     dp.score_stride = stride;
     dp.early_kv = early_kv_ok(c, layer, s) ? 1 : 0;
     if (!c->pdl) dp.deep_pipeline = 0;

@@ -116,7 +116,8 @@ struct DecodeRow {
   int32_t ctr;          // row index of this row's merge tickets
   int32_t split_tiles;  // segment 0 tiles (kTileKeys keys) per split
   int32_t split_tiles2; // segment 1 (hybrid ring; keys min(pos + 1, ring_R)) tiles per split
-  uint16_t call_row;    // < kMaxRowsPerLaunch
+  uint16_t call_row;    // row of q, out and the new keys from the launch's first row's on (a
+                        // list launch: token)
   uint16_t item0;       // first work item of this row (< kMaxRowsPerLaunch * kMaxSplits)
   uint16_t part0;       // first partial slot of this row (items of multi-split rows)
   uint8_t n_splits;     // segment 0 splits
