@@ -510,7 +510,8 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
  * kv_append_weights: kv_append on a KV_GLOBAL layer (same q, k, v, n_new, rows, out, effects
  *   and errors) that also counts which keys the new tokens attend to.  acc_in, acc_out:
  *   device float [B][Hk][max_len], an accumulator per cache row, kv head and storage slot
- *   that the caller owns, 4-byte aligned; the same buffer, or two that do not overlap.  For
+ *   that the caller owns, 4-byte aligned; the same buffer, or two that do not overlap
+ *   (KV_ERR_ARG if they do).  For
  *   every row with n = n_new[i] > 0 and slots s before the call, kv head g and slot
  *   j < s + n:
  *     acc_out[row][g][j] = (j < s ? acc_in[row][g][j] : 0)

@@ -2790,6 +2790,9 @@ int kv_append_weights(kv_cache *c, int layer, const void *q, const void *k, cons
       !aligned16(v) || !aligned16(out) ||
       ((reinterpret_cast<uintptr_t>(acc_in) | reinterpret_cast<uintptr_t>(acc_out)) & 3u))
     return KV_ERR_ARG;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(acc_in), b = reinterpret_cast<uintptr_t>(acc_out);
+  if (a != b && std::max(a, b) - std::min(a, b) < (size_t)c->B * c->Hk * c->max_len * 4)
+    return KV_ERR_ARG;  // a CTA would read what another has written
   DeviceGuard guard(c->device);
   cudaStream_t s = (cudaStream_t)stream;
   rc = ensure_weights_room(c);

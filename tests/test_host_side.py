@@ -119,3 +119,18 @@ def test_a_first_counting_call_may_be_captured(lib):
     assert lib.fake_bad_mallocs() == 0                 # none under a mode that refuses them
     lib.fake_reset()
     c.close()
+
+
+def test_accumulators_that_overlap_in_part_are_refused(lib):
+    c = Cache(lib)                                     # accumulators of 2 x 2 x 640 floats
+    c.fill([100, 0])
+    names(c)
+    size = 2 * 2 * 640 * 4
+    for d in (4, 640 * 4, size - 4):
+        for a, b in ((0, d), (d, 0)):
+            assert c.weights([1, 20], host_side.PTR + a, host_side.PTR + b) == 1
+    assert names(c) == []
+    assert c.weights([1, 20], host_side.PTR, host_side.PTR + size) == 0
+    assert c.weights([1, 20], host_side.PTR + size, host_side.PTR) == 0
+    assert c.weights([1, 20], host_side.PTR, host_side.PTR) == 0
+    c.close()
