@@ -539,9 +539,10 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
  *   acc_out: NULL, or such an array for `dst` ([dst B][Hk][dst max_len]) with NULL where
  *     not wanted: the kept keys' accumulators, moved with them (a zero's sign and a NaN's
  *     payload may change).  acc_out[l] may be acc_in[l]
- *     when dst == src; else the two must not overlap.
+ *     when dst == src; but for that, no acc_out[l] overlaps any acc_in or another acc_out.
  *   kept: host array [n_layers] of device int32 [n][Hk][keep], set for the global layers:
- *     receives the source slots of destination slots 0.., -1 past the last.
+ *     receives the source slots of destination slots 0.., -1 past the last.  Overlaps none
+ *     of the accumulators and no other layer's.
  *   1 <= keep <= both caches' max_len, 0 <= recent <= keep.  dst may be src, and a row its
  *   own destination (cut in place; a paged row's blocks past the kept keys return to the
  *   pool; blocks that other rows hold too are copied first, which takes free blocks).  Rows,

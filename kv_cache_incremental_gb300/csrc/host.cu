@@ -7,6 +7,7 @@
 // first enqueue, so a rejected call changes nothing (pycraft-1 `update` guards;
 // "KV cache full" is raised before any write in tiny_agent/generate.py
 // `append`).
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -2823,6 +2824,37 @@ namespace {
 // item (32 rows x 8 heads x 512 positions, D = 128: 25.8 us in whole rings).
 constexpr int kRingSpan = 128;
 
+// Whether a buffer that an eviction writes (acc_out, kept) overlaps another one that it reads or
+// writes.  acc_out[l] may be acc_in[l] in one cache: a row's weights are then moved in place.
+bool evict_overlaps(const kv_cache *dst, const kv_cache *src, const std::vector<int> &layers, int n,
+                    int keep, const float *const *acc_in, float *const *acc_out,
+                    int32_t *const *kept) {
+  struct Range {
+    uintptr_t a, b;
+    bool written;
+  };
+  std::vector<Range> ranges;
+  const auto add = [&](const void *p, int64_t words, bool written) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    ranges.push_back({a, a + 4 * (uintptr_t)words, written});
+  };
+  for (int l : layers) {
+    const float *out = acc_out ? acc_out[l] : nullptr;
+    if (out) add(out, (int64_t)dst->B * dst->Hk * dst->max_len, true);
+    if (!(dst == src && out == acc_in[l]))
+      add(acc_in[l], (int64_t)src->B * src->Hk * src->max_len, false);
+    add(kept[l], (int64_t)n * dst->Hk * keep, true);
+  }
+  std::sort(ranges.begin(), ranges.end(), [](const Range &x, const Range &y) { return x.a < y.a; });
+  uintptr_t end_read = 0, end_written = 0;  // of the ranges that start before
+  for (const Range &r : ranges) {
+    if (r.a < end_written || (r.written && r.a < end_read)) return true;
+    uintptr_t &end = r.written ? end_written : end_read;
+    end = std::max(end, r.b);
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -2865,6 +2897,7 @@ int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
       for (int j = 0; j < n; ++j)
         if (i != j && dst_rows[i] == src_rows[j]) return KV_ERR_ARG;
   if (n == 0) return KV_OK;
+  if (evict_overlaps(dst, src, layers, n, keep, acc_in, acc_out, kept)) return KV_ERR_ARG;
   DeviceGuard guard(dst->device);
   cudaStream_t s = (cudaStream_t)stream;
   std::vector<int32_t> slots(n), m(n), lens(n);

@@ -134,3 +134,37 @@ def test_accumulators_that_overlap_in_part_are_refused(lib):
     assert c.weights([1, 20], host_side.PTR + size, host_side.PTR) == 0
     assert c.weights([1, 20], host_side.PTR, host_side.PTR) == 0
     c.close()
+
+
+def test_eviction_buffers_that_overlap_are_refused(lib):
+    a = Cache(lib, kinds=(0, 1, 0), W=8)               # accumulators of 2 x 2 x 640 floats
+    b = Cache(lib, kinds=(0, 1, 0), W=8)
+    a.fill([300, 200])
+    P, acc, kept = host_side.PTR, 2 * 2 * 640 * 4, 2 * 2 * 100 * 4
+    was = a.state(), b.state()
+    names(a)
+
+    def call(dst, acc_in, acc_out, kept_):
+        full = lambda x: None if x is None else [x[0], None, x[1]]
+        return dst.evict([0, 1], a, [0, 1], 100, 9, full(acc_in), full(acc_out), full(kept_))
+
+    A, B, C, D = (P + i * acc for i in range(4))       # next to one another
+    K, L = P + 4 * acc, P + 4 * acc + kept
+    for dst, args in (
+            (b, ((A, B), (A, C), (K, L))),             # another cache: rows lie elsewhere
+            (b, ((A, B), (C, B + 4), (K, L))),
+            (a, ((A, B), (C, C), (K, L))),             # two layers written to one buffer
+            (a, ((A, A), (A, C), (K, L))),             # one layer's weights read and written
+            (a, ((A, B), (B, A), (K, L))),             # each layer's into the other's
+            (a, ((A, B), (A + 4, C), (K, L))),         # in part
+            (a, ((A, B), None, (K, K + 4))),           # kept lists
+            (a, ((A, B), None, (K, B + acc - 4))),
+            (a, ((A, B), (C, D), (K, D + acc - 4)))):
+        assert call(dst, *args) == 1, args
+    assert names(a) == [] and (a.state(), b.state()) == was
+    for dst, args in ((b, ((A, B), (C, D), (K, L))), (a, ((A, B), (A, B), (K, L))),
+                      (a, ((A, B), (C, D), (L, K))), (b, ((A, A), None, (K, L))),
+                      (b, ((A, A + 8), (None, D), (K, L)))):
+        assert call(dst, *args) == 0, args
+    a.close()
+    b.close()
