@@ -2526,16 +2526,16 @@ int kv_sparse_enable(kv_cache *c, int max_select) try {
   kv_cache::Sparse sp;
   sp.nb_cap = std::max(1, c->max_len / kSparseBlock);
   const size_t blocks = (size_t)c->B * c->Hk * sp.nb_cap;
+  // all host memory first: nothing below throws
+  sp.bound.assign(c->n_layers, nullptr);
+  sp.scale.assign(c->n_layers, nullptr);
+  for (int l = 0; l < c->n_layers; ++l)
+    sp.valid.push_back(std::vector<int32_t>(c->kind[l] == KV_GLOBAL ? c->B : 0, 0));
   bool ok = true;
   for (int l = 0; l < c->n_layers; ++l) {
-    void *b = nullptr, *f = nullptr;
-    if (c->kind[l] == KV_GLOBAL) {
-      ok = ok && cudaMalloc(&b, blocks * 2 * c->D) == cudaSuccess;
-      ok = ok && cudaMalloc(&f, blocks * 4) == cudaSuccess;
-    }
-    sp.bound.push_back((int8_t *)b);
-    sp.scale.push_back((float *)f);
-    sp.valid.push_back(std::vector<int32_t>(c->kind[l] == KV_GLOBAL ? c->B : 0, 0));
+    if (c->kind[l] != KV_GLOBAL) continue;
+    ok = ok && cudaMalloc((void **)&sp.bound[l], blocks * 2 * c->D) == cudaSuccess;
+    ok = ok && cudaMalloc((void **)&sp.scale[l], blocks * 4) == cudaSuccess;
   }
   const size_t lists = (size_t)kMaxSelectQueries * c->Hk * max_select * 4;
   const size_t tickets = (size_t)kMaxRowsPerLaunch * c->Hk * 4;
@@ -2553,7 +2553,7 @@ int kv_sparse_enable(kv_cache *c, int max_select) try {
     return have ? KV_ERR_CUDA : KV_ERR_OOM;
   }
   sp.max_select = max_select;
-  c->sparse = sp;
+  c->sparse = std::move(sp);
   return KV_OK;
 } catch (...) {  // host memory
   return KV_ERR_OOM;

@@ -168,3 +168,26 @@ def test_eviction_buffers_that_overlap_are_refused(lib):
         assert call(dst, *args) == 0, args
     a.close()
     b.close()
+
+
+@pytest.mark.parametrize("which", ["fake_fail_new", "fake_fail_malloc"])
+def test_enabling_sparse_attention_without_memory_leaves_nothing_behind(lib, which):
+    """Every allocation of the call, on the host or on the device, is the one that fails once."""
+    nth = 0
+    while True:
+        c = Cache(lib, kinds=(0, 1, 0), W=8)
+        held = lib.fake_live_bytes(), lib.fake_live_blocks()
+        lib.fake_reset()
+        getattr(lib, which)(nth)
+        rc = lib.kv_sparse_enable(c.h, 4)
+        lib.fake_reset()
+        if rc == 0:
+            assert nth >= 6                            # two layers' bounds, lists, tickets
+            c.close()
+            break
+        assert rc == 5 and (lib.fake_live_bytes(), lib.fake_live_blocks()) == held, nth
+        assert c.sparse([1, 1], 1) == 1                # still not enabled
+        assert lib.kv_sparse_enable(c.h, 4) == 0
+        c.close()
+        assert lib.fake_live_blocks() == 0
+        nth += 1
