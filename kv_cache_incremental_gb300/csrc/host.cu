@@ -236,6 +236,13 @@ void drop_block(kv_cache *c, int blk) {
   if (--c->refs[blk] == 0) c->free_blocks.push_back(blk);
 }
 
+// Host memory for `n` blocks of a row, ahead of a change of the pool: taking them then throws
+// nothing.  (At least doubled, as the vector itself would.)
+void reserve_blocks(kv_cache *c, int row, int n) {
+  auto &rb = c->rblocks[row];
+  if ((size_t)n > rb.capacity()) rb.reserve(std::max((size_t)n, 2 * rb.capacity()));
+}
+
 // Give each (row, length) of `want` the pool blocks its first `length` positions need, and
 // write the new table entries on `s`.  All or nothing: KV_ERR_POOL before any change if the
 // pool cannot supply every row.
@@ -245,6 +252,7 @@ int ensure_blocks(kv_cache *c, const std::vector<std::pair<int, int>> &want, cud
   for (auto &w : want) need += std::max(0, blocks_for(w.second) - (int)c->rblocks[w.first].size());
   if (need > (int64_t)c->free_blocks.size()) return KV_ERR_POOL;
   if (need == 0) return KV_OK;
+  for (auto &w : want) reserve_blocks(c, w.first, blocks_for(w.second));
   static thread_local TableParams tp;
   tp.table = c->table;
   tp.max_blocks = c->max_blocks;
@@ -2907,6 +2915,14 @@ int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
     slots[i] = slots_of(src, src_rows[i]);
     m[i] = std::min(slots[i], keep);
   }
+  std::vector<int32_t> moved, moved_lens;  // rows that are not cut in place, and their lengths
+  std::vector<std::pair<int, int>> want;   // and, paged, the slots they need blocks for
+  for (int i = 0; i < n; ++i)
+    if (!in_place(i)) {
+      moved.push_back(dst_rows[i]);
+      moved_lens.push_back(lens[i]);
+      want.push_back({dst_rows[i], m[i]});
+    }
   // Pool blocks, all or nothing before anything is enqueued.  A row cut in place keeps its
   // first blocks, with copies of those that other rows hold too (the kept keys are moved
   // into them), and lets go of the others when the keys have moved; any other destination
@@ -2934,6 +2950,8 @@ int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
       }
     }
     if (avail < 0) return KV_ERR_POOL;
+    for (const auto &w : want) reserve_blocks(dst, w.first, blocks_for(w.second));
+    // from here on no host memory is asked for: the rows change as a whole
     static thread_local TableParams tp;
     static thread_local CopyParams cp;
     tp.table = dst->table;
@@ -2942,12 +2960,7 @@ int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
     cp.Hk = dst->Hk;
     cp.D = dst->D;
     cp.n_items = 0;
-    std::vector<std::pair<int, int>> want;
-    for (int i = 0; i < n; ++i)
-      if (!in_place(i)) {
-        release_blocks(dst, dst_rows[i], 0);
-        want.push_back({dst_rows[i], m[i]});
-      }
+    for (int d : moved) release_blocks(dst, d, 0);
     int rc = KV_OK;
     for (int i = 0; i < n && rc == KV_OK; ++i) {
       if (!in_place(i) || slots[i] <= keep) continue;
@@ -2991,12 +3004,6 @@ int kv_evict_rows(kv_cache *dst, const int32_t *dst_rows, const kv_cache *src,
   cp.D = dst->D;
   cp.n_items = 0;
   cp.beside = dst->pdl ? 1 : 0;
-  std::vector<int32_t> moved, moved_lens;
-  for (int i = 0; i < n; ++i)
-    if (!in_place(i)) {
-      moved.push_back(dst_rows[i]);
-      moved_lens.push_back(lens[i]);
-    }
   const auto copy_rings = [&]() -> int {
     for (int i = 0; i < n; ++i) {
       if (in_place(i)) continue;

@@ -191,3 +191,65 @@ def test_enabling_sparse_attention_without_memory_leaves_nothing_behind(lib, whi
         c.close()
         assert lib.fake_live_blocks() == 0
         nth += 1
+
+
+def evictions():
+    """Paged rows 0 and 1 share blocks, row 2 has its own; (destination rows, source rows)."""
+    return [([0, 2], [0, 2]), ([0, 2], [0, 1]), ([2, 1], [0, 1]), ([1], [2])]
+
+
+@pytest.mark.parametrize("dst,src", evictions())
+def test_evictions_without_host_memory_change_nothing(lib, dst, src):
+    """Every host allocation of the call is the one that fails once."""
+    P = host_side.PTR
+    nth = 0
+    while True:
+        c = Cache(lib, B=3, kinds=(0, 1, 0), W=8, blocks=80)
+        c.fill([300, 0, 130])
+        assert lib.kv_copy_rows(c.h, host_side.i32([1]), c.h, host_side.i32([0]), None, 1,
+                                None) == 0
+        was = c.state()
+        names(c)
+        call = lambda: c.evict(dst, c, src, 100, 9, [P, None, P + (1 << 24)], None,
+                               [P + (2 << 24), None, P + (3 << 24)])
+        lib.fake_fail_new(nth)
+        rc = call()
+        lib.fake_fail_new(-1)
+        if rc == 0:
+            # the first allocations of a launch's parameter blocks are made once per thread
+            assert nth >= 10
+            c.close()
+            break
+        assert rc == 5 and names(c) == [] and c.state() == was, nth
+        assert call() == 0
+        slots = c.state()[1]
+        assert [slots[d] for d in dst] == [min(100, was[1][s]) for s in src]
+        c.close()
+        nth += 1
+    lib.fake_reset()
+
+
+def test_appends_that_run_out_of_host_memory_lose_no_block(lib):
+    """A call that appends to paged rows and fails may have given them their blocks already
+    (the call made again needs no others), but every block is free or some row's."""
+    for call in (lambda c: c.sparse([1, 70, 1], 2), lambda c: c.weights([1, 70, 1], last=9)):
+        nth = 0
+        while True:
+            c = Cache(lib, B=3, blocks=80)
+            c.fill([304, 0, 128])                      # whole blocks: the next token needs one
+            assert lib.kv_sparse_enable(c.h, 8) == 0
+            lens = c.state()[0]
+            lib.fake_fail_new(nth)
+            rc = call(c)
+            lib.fake_fail_new(-1)
+            now, _, tables, free = c.state()
+            assert free + sum(map(len, tables)) == 80 and now == lens, nth
+            held = [b for t in tables for b in t]
+            assert len(set(held)) == len(held)
+            if rc != 0:
+                assert rc == 5 and call(c) == 0
+            c.close()
+            nth += 1
+            if rc == 0:
+                break
+    lib.fake_reset()
