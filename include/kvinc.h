@@ -31,7 +31,11 @@
  * Conventions for every entry point:
  *  - Return value: KV_OK or a kv_status code; kv_strerror() names it.
  *  - Every argument is validated on the host before any work is enqueued; a
- *    call that returns an error has changed no state (host or device).
+ *    call that returns an error has changed no state (host or device).  Two errors can come
+ *    after part of a call's work was enqueued: KV_ERR_CUDA (a launch failed) and, from a call
+ *    that appends, a KV_ERR_OOM of host memory.  No row's length has changed then; the new
+ *    tokens' slots, the call's outputs and an accumulator it adds to in place hold anything,
+ *    and so does a destination row of a copy, an import or an eviction until it is reset.
  *  - Device work runs asynchronously on the caller's CUDA stream (`stream`,
  *    a cudaStream_t passed as void*, NULL = legacy default stream).  No entry
  *    point synchronises the device unless its comment says so.
@@ -479,7 +483,8 @@ int kv_import_row(kv_cache *c, int row, int keep, const void *src, int64_t bytes
  * operations, and the block's the largest over the group's Hq / Hk heads.  (A largest
  * magnitude below 1e-30 counts as 0.)  The sum is a whole number, so the choice does not
  * depend on the order of additions; ties go to the lower block, NaN scores below all
- * others.
+ * others.  (A block with an infinite or NaN key component may score anything; a call still
+ * reads valid blocks of its row.)
  *
  * kv_sparse_enable: prepares a cache with at least one KV_GLOBAL layer for calls of up to
  *   max_select (1..4096) blocks per query: allocates, for every global layer, the bounds
@@ -533,7 +538,10 @@ int kv_append_sparse(kv_cache *c, int layer, const void *q, const void *k, const
  *   0..keep-1.  A row with keep slots or fewer keeps them all.  Sliding layers keep their
  *   rings.  The row's length and positions do not change: a later token is rotated at its
  *   true position, attends to the kept keys at theirs, and goes to the next free slot
- *   (kv_get_slots), while kv_append and the other calls that append go on as before.
+ *   (kv_get_slots), while kv_append and the other calls that append go on as before -- up to
+ *   max_len positions, whatever the slots in use: max_len bounds both, so a source row must
+ *   have at most dst's max_len positions, and a dense cache holds as much memory as before
+ *   (what eviction saves there is the reading; a paged row's blocks go back to the pool).
  *   acc_in: host array [n_layers] of device float [src B][Hk][src max_len], set for the
  *     global layers (entries of others are ignored).
  *   acc_out: NULL, or such an array for `dst` ([dst B][Hk][dst max_len]) with NULL where

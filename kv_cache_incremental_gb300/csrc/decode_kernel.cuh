@@ -59,8 +59,9 @@ constexpr int kMiniRows = 16;  // rows of the new-key mini-tile
 // with chunks of up to 64 tokens over 19 blocks, the whole call: 101.7 -> 96.3 us; at D = 128
 // two stages and three CTAs lost, 16 rows over 37 blocks 40.4 -> 42.8).  LIST with DEEP: five
 // (six) stages, so that more of the blocks known before the selection stream while it runs (16
-// rows over 37 blocks, 128 CTAs: 41.1 us with three stages, 37.8 with four or five, 38.2 with
-// six; 64 rows over 19 blocks, 512 CTAs, would go from 58.5 to 67).
+// rows over 37 blocks, 128 CTAs, D = 128: 41.1 us with three stages, 37.8 with four or five, 38.2
+// with six; 64 rows over 19 blocks, 512 CTAs, would go from 58.5 to 67; D = 64, 36 rows x 4 heads
+// over 37 blocks: 31.5 with three, 28.7 with four, 26.7 with six, 26.6 with eight).
 template <int D, bool DEEP, bool LIST = false>
 struct DecodeCfg {
   static constexpr int kPanels = D / 64;                        // 128-byte swizzle panels

@@ -103,7 +103,8 @@ struct AppendParams {
 };
 
 // ---------------------------------------------------------------- decode
-// Keys of a decode row: segment 0 (storage slots [0, nk) of the layer storage) and, for a
+// Keys of a decode row: segment 0 (storage slots [0, nk) of the layer storage; a list launch:
+// the row's listed blocks, DecodeParams::list) and, for a
 // hybrid layer, segment 1 (its ring, slots [0, nk2)); each segment has its own splits, and
 // the items of segment 1 follow those of segment 0.  All splits merge into one output.
 // One decode row, 32 bytes: the parameter block (all rows of a launch) is fetched on every
@@ -115,7 +116,8 @@ struct DecodeRow {
   int32_t nk;           // segment 0: storage slots [0, nk)
   int32_t ctr;          // row index of this row's merge tickets
   int32_t split_tiles;  // segment 0 tiles (kTileKeys keys) per split
-  int32_t split_tiles2; // segment 1 (hybrid ring; keys min(pos + 1, ring_R)) tiles per split
+  int32_t split_tiles2; // segment 1 (hybrid ring; keys min(pos + 1, ring_R)) tiles per split;
+                        // a list launch: the index of the row's last block
   uint16_t call_row;    // row of q, out and the new keys from the launch's first row's on (a
                         // list launch: token)
   uint16_t item0;       // first work item of this row (< kMaxRowsPerLaunch * kMaxSplits)
@@ -146,8 +148,10 @@ struct DecodeParams {  // 64-byte aligned through its CUtensorMap members
   int64_t kv_row_stride;
   __nv_bfloat16 *cache_k;      // layer storage [B][Hk][seg_rows][D]
   __nv_bfloat16 *cache_v;
-  int fuse_append;          // the new key goes to segment 0 at slot pos (global) or
-  int seg0_ring;            // pos % ring_R (seg0_ring = 1: a sliding layer's ring)
+  // fuse_append = 1: the new key goes to segment 0, at its last slot nk - 1 (a cache: slot pos
+  // less the row's evicted keys) or, with seg0_ring (a sliding layer's ring), at pos % ring_R
+  int fuse_append;
+  int seg0_ring;
   int ring_R;
   int Hq, Hk, rep, seg_rows;
   int n_rows, n_items;
@@ -347,8 +351,8 @@ struct BoundsParams {
   BoundsRow rows[kMaxRowsPerLaunch];
 };
 
-// One query token whose blocks are chosen per kv head.
-// The query tokens of one row in a launch; those of a chunk follow one another.
+// The query tokens of one row in a launch; those of a chunk follow one another.  Their blocks
+// are chosen per kv head.
 struct SelectRow {
   int32_t cache_row;
   int32_t slot;         // storage slot of the first token's own key
