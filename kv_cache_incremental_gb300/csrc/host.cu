@@ -315,11 +315,22 @@ void note_launch(kv_cache *c, cudaStream_t s, int kind) {
   c->last_layer = c->cur_layer;
 }
 
+// Room for one more record, or none: a launch is made whether or not it can be recorded.
+bool room_for_record(kv_cache *c) noexcept {
+  if (c->recs.size() < c->recs.capacity()) return true;
+  try {
+    c->recs.reserve(std::max<size_t>(64, 2 * c->recs.capacity()));
+  } catch (...) {
+    return false;
+  }
+  return true;
+}
+
 // Launch `fn` with an optional event pair around it.
 template <class F>
 cudaError_t timed(kv_cache *c, int kind, double bytes, double flops, cudaStream_t s, F fn) {
   note_launch(c, s, kind);
-  if (!c->prof || c->recs.size() >= kMaxProfRecs) return fn();
+  if (!c->prof || c->recs.size() >= kMaxProfRecs || !room_for_record(c)) return fn();
   ProfRec r{take_event(c), take_event(c), kind, bytes, flops};
   if (!r.a || !r.b) return fn();
   cudaEventRecord(r.a, s);

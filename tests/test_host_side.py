@@ -198,8 +198,9 @@ def evictions():
     return [([0, 2], [0, 2]), ([0, 2], [0, 1]), ([2, 1], [0, 1]), ([1], [2])]
 
 
+@pytest.mark.parametrize("profile", [0, 1])
 @pytest.mark.parametrize("dst,src", evictions())
-def test_evictions_without_host_memory_change_nothing(lib, dst, src):
+def test_evictions_without_host_memory_change_nothing(lib, dst, src, profile):
     """Every host allocation of the call is the one that fails once."""
     P = host_side.PTR
     nth = 0
@@ -208,6 +209,7 @@ def test_evictions_without_host_memory_change_nothing(lib, dst, src):
         c.fill([300, 0, 130])
         assert lib.kv_copy_rows(c.h, host_side.i32([1]), c.h, host_side.i32([0]), None, 1,
                                 None) == 0
+        assert lib.kv_profile_enable(c.h, profile) == 0
         was = c.state()
         names(c)
         call = lambda: c.evict(dst, c, src, 100, 9, [P, None, P + (1 << 24)], None,
@@ -215,8 +217,7 @@ def test_evictions_without_host_memory_change_nothing(lib, dst, src):
         lib.fake_fail_new(nth)
         rc = call()
         lib.fake_fail_new(-1)
-        if rc == 0:
-            # the first allocations of a launch's parameter blocks are made once per thread
+        if rc == 0:     # also when it is a launch's record that found no memory
             assert nth >= 10
             c.close()
             break
