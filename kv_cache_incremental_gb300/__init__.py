@@ -279,7 +279,8 @@ class KVCache:
         """append() on a global layer that adds the softmax weights of each row's last `last`
         (default: all) new tokens to a per-key accumulator: float32 tensors (B, Hk, max_len),
         acc_out = acc_in (0 for the new keys) + weights; the same tensor or two that do not
-        overlap.  See kv_append_weights in include/kvinc.h."""
+        overlap.  A cache's first call allocates the memory that counting needs.  See
+        kv_append_weights in include/kvinc.h."""
         import torch
         self._check_tensor(q, "q", self.Hq)
         Bs, C = q.shape[:2]

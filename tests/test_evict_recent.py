@@ -1,6 +1,6 @@
 """Evictions that keep the last slots only (recent == keep), the plain sliding cut: no slot
 competes, so every kept weight is one that the choice's CTA has only just read.  Rows of
-several load rounds (8192 slots each), held in shared memory and longer than that, into other
+several load passes (8192 slots each), held in shared memory and longer than that, into other
 rows and in place; the moved accumulators are compared exactly."""
 import numpy as np
 import pytest

@@ -59,3 +59,12 @@ def test_an_ordinary_cache_holds_no_room_for_scores():
         D * 4 + 8)
     assert before - free() <= kv + rest + (16 << 20)   # allocations are rounded up
     c.close()
+
+
+@pytest.mark.parametrize("Hk,rep,D", [(2, 4, 64), (2, 2, 128), (1, 16, 128)])
+def test_chunks_whose_last_token_stands_alone(Hk, rep, D):
+    """A first call whose rows end in a sub-chunk of one token, the only one counted: nothing is
+    read that the attention has not left."""
+    r = Rows(3, 800, Hk * rep, Hk, D, [300, 0, 129], seed=6)
+    test_weights.step(r, [65, 129, 1], 1)
+    test_weights.step(r, [65, 1, 193], 2)
