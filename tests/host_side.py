@@ -3,6 +3,7 @@ the build leaves are linked with it into a library of their own.  Pointers that 
 device buffers are plain numbers that nobody follows."""
 import ctypes
 import os
+import shutil
 import subprocess
 
 from kv_cache_incremental_gb300 import _build, _lib
@@ -15,8 +16,8 @@ def build(directory):
     objs = [os.path.join(_build.OUT_DIR, s.replace(".cu", ".o")) for s in _build.SOURCES]
     _build.build(force=not all(map(os.path.exists, objs)))
     out = os.path.join(directory, "libkvinc_host.so")
-    nvcc = subprocess.run(["which", "nvcc"], capture_output=True, text=True).stdout.strip()
-    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    nvcc = os.path.realpath(shutil.which("nvcc"))
+    include = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
     r = subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-Wl,-Bsymbolic",
                         "-Wl,-z,defs", f"-I{include}", os.path.join(HERE, "fake_cudart.cpp"),
                         *objs, "-o", out], capture_output=True, text=True)
