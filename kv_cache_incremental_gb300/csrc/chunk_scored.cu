@@ -29,6 +29,10 @@
 // of them take that.  (Values are looked at only then: a scan of every tile would be on the
 // chain.)
 //
+// A piece of a split row's keys may hold no block for a query tile.  Such a CTA has no MMAs to wait
+// for, so it commits none either: a commit's arrival that nothing waits for could come after the
+// CTA's end, in shared memory that is the next CTA's.
+//
 // Warps: 0-15 softmax (quarter of the block, 32 rows); 16 and 19 load K and V; 17 (which owns
 // TMEM) issues the MMAs of S, 18 those of O.  Each is one thread's work: a TMA box takes its
 // issuer about 200 cycles, an MMA 60 to 100, and a read of shared memory after MMAs stalls for
@@ -368,7 +372,7 @@ __device__ __forceinline__ void s_run(const ScoredPrefillParams &p, uint8_t *sme
     if (++buf == kBufs) buf = 0, o_phase ^= 1;
   }
   if (!ok) give_up<D>(p, smem);
-  tc::commit(bar.drain());
+  if (n_blocks > 0) tc::commit(bar.drain());  // (without a block no one waits for it)
 }
 
 // The MMAs of O of a run: one thread.
@@ -399,7 +403,7 @@ __device__ __forceinline__ void o_run(const ScoredPrefillParams &p, uint8_t *sme
     if (++buf == kBufs) buf = 0, p_phase ^= 1;
   }
   if (!ok) give_up<D>(p, smem);
-  tc::commit(bar.drain());
+  if (n_blocks > 0) tc::commit(bar.drain());  // (without a block no one waits for it)
 }
 
 // What a softmax thread's query row sees: positions from `first` to `pos` (a tree: all cached ones
