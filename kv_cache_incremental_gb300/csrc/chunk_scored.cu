@@ -844,7 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = fl->tmem;
 
   if (soft) {
-    // The rotated queries into the 128-byte-swizzled Q tile.
+    // The rotated queries into the 128-byte-swizzled Q tile, times a power of two.
+    const float qs = p.q_scale;
     uint8_t *q_tile = smem + C::kOff_Q;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -859,10 +860,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float4 e = cs[j];
         const float a0 = __uint_as_float(w1[j] << 16), a1 = __uint_as_float(w1[j] & 0xffff0000u);
         const float b0 = __uint_as_float(w2[j] << 16), b1 = __uint_as_float(w2[j] & 0xffff0000u);
-        w1[j] = ptx::pack_bf16(__fsub_rn(__fmul_rn(a0, e.x), __fmul_rn(b0, e.y)),
-                               __fsub_rn(__fmul_rn(a1, e.z), __fmul_rn(b1, e.w)));
-        w2[j] = ptx::pack_bf16(__fadd_rn(__fmul_rn(a0, e.y), __fmul_rn(b0, e.x)),
-                               __fadd_rn(__fmul_rn(a1, e.w), __fmul_rn(b1, e.z)));
+        w1[j] = ptx::pack_bf16(qs * __fsub_rn(__fmul_rn(a0, e.x), __fmul_rn(b0, e.y)),
+                               qs * __fsub_rn(__fmul_rn(a1, e.z), __fmul_rn(b1, e.w)));
+        w2[j] = ptx::pack_bf16(qs * __fadd_rn(__fmul_rn(a0, e.y), __fmul_rn(b0, e.x)),
+                               qs * __fadd_rn(__fmul_rn(a1, e.w), __fmul_rn(b1, e.z)));
       }
       const int c_hi = kPairs + c;  // 16-byte chunks along D
       *reinterpret_cast<uint4 *>(q_tile + (c / 8) * kRows * 128 + ptx::swz128(qr, c % 8)) = x1[i];

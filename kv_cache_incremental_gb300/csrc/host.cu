@@ -2946,6 +2946,16 @@ void set_cap(float cap, int D, float &cap_in, float &cap_out) {
   cap_out = (float)(1.4426950408889634 * cap);
 }
 
+// As set_cap, for chunk_scored.cu, whose capped scores are polynomials of the products with
+// coefficients down to 0.0155 cap_in^9 cap_out: some way below cap_in = 2^-14 (a cap of 1448 at
+// D = 128) that leaves the normal floats.  So larger caps take queries times a power of two (at
+// most 7 halvings; exact in bf16) and as much larger a cap_in.
+constexpr float kMinCapIn = 1.f / 16384;
+void set_cap_scaled(float cap, int D, float &cap_in, float &cap_out, float &q_scale) {
+  set_cap(cap, D, cap_in, cap_out);
+  for (q_scale = 1.f; cap_in > 0.f && cap_in < kMinCapIn; q_scale *= 0.5f) cap_in *= 2.f;
+}
+
 // Tokens of a row in one launch, with changed scores: `row` as ScoredPrefillParams has it.
 struct ScoredEntry {
   PrefillRow row;
@@ -3074,7 +3084,7 @@ int attend_scored(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat16 
   p.part_o = c->ppart_o;
   p.part_ml = c->ppart_ml;
   p.ml_out = nullptr;
-  set_cap(sa.cap, D, p.cap_in, p.cap_out);
+  set_cap_scaled(sa.cap, D, p.cap_in, p.cap_out, p.q_scale);
   p.slopes = sa.slopes;
   p.first = sa.first;
   p.parents = sa.parents;

@@ -262,7 +262,9 @@ struct PrefillParams {  // 64-byte aligned through its CUtensorMap members
 // keys are stored before.  With `first` on such a layer an entry is piece tile0 of tile1 equal shares
 // of the key blocks that count.
 struct ScoredPrefillParams : PrefillParams {
-  float cap_in, cap_out;   // as ScoredDecodeParams
+  // Queries are multiplied by q_scale, a power of two, as they are rotated (1 without a cap);
+  // cap_in, cap_out: as ScoredDecodeParams, for the products of those.
+  float cap_in, cap_out, q_scale;
   const float *slopes;
   const int32_t *first;    // per token: its first visible position, or nullptr
   const int32_t *parents;  // drafted trees: per token its parent's index in the row; or nullptr.

@@ -41,8 +41,8 @@ __device__ __forceinline__ float tanh_any(float x) {
 
 // The polynomial r, of N coefficients, of a capped score cap_out tanh(v cap_in) = v r(v^2) while |v|
 // cap_in <= kTanhSmall (N = 5) or kTanhTiny (4), for two scores at a time: N packed instructions.
-// Its coefficients hold powers of cap_in up to the eighth; the host admits caps for which none of
-// them that counts underflows.
+// Its coefficients hold powers of cap_in up to the ninth; the host scales the products v so that all
+// of them are normal floats (kMinCapIn).
 template <int N>
 struct CapSmall {
   uint64_t c[N];
