@@ -3040,7 +3040,12 @@ int attend_scored(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat16 
   const bool shares = sa.first && !sliding;
   std::vector<ScoredEntry> ents;
   std::vector<MergeRow> merges;
-  std::vector<std::pair<int, int>> order;  // (minus the length, entry): the longest ones first
+  std::vector<std::pair<int, int>> order;  // (minus the length, entry)
+  // Launches are [ends[i - 1], ends[i]) of `order`, in each the longest entries first.  The pieces that
+  // a ticket counts are in one: a launch is refused as a whole, and tickets stay zero between calls.
+  std::vector<size_t> ends;
+  size_t launch0 = 0;
+  int ctas = 0;
   int64_t part = 0;
   for (ScoredEntry e : in) {
     int len;
@@ -3050,6 +3055,14 @@ int attend_scored(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat16 
     e.part0 = (int32_t)part;
     e.splits = ticketed ? ns : 0;
     for (int i = 0; i < ns; ++i) {
+      const int more = !ticketed ? 1 : i == 0 ? ns : 0;  // entries that go together from here on
+      if (ents.size() - launch0 + more > kMaxRowsPerLaunch ||
+          ctas + more * ctas_of(e) > kMaxEntryCtas) {
+        ends.push_back(ents.size());
+        launch0 = ents.size();
+        ctas = 0;
+      }
+      ctas += ctas_of(e);
       e.row.tile0 = shares ? i : 2 * len * i;
       e.row.tile1 = shares ? ns : i == ns - 1 ? INT32_MAX : 2 * len * (i + 1);
       e.row.part = ns > 1 ? (int32_t)part : -1;
@@ -3058,7 +3071,7 @@ int attend_scored(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat16 
       ents.push_back(e);
     }
   }
-  std::sort(order.begin(), order.end());
+  ends.push_back(ents.size());
   p.tmap_k = p.tmap_k2 = c->tmK[layer];
   p.tmap_v = p.tmap_v2 = c->tmV[layer];
   p.tmap_k16 = c->tmK16[layer];
@@ -3090,22 +3103,23 @@ int attend_scored(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat16 
   p.parents = sa.parents;
   p.counters = c->counters;
   p.rep_inv = rep == 1 ? 0 : (uint32_t)(((1ULL << 32) + rep - 1) / rep);
-  for (size_t r0 = 0, r1; r0 < ents.size(); r0 = r1) {
+  size_t r0 = 0;
+  for (const size_t r1 : ends) {
     int cta = 0;
     double bytes = 0, fl = 0;
+    std::sort(order.begin() + r0, order.begin() + r1);
     p.uniform_tiles = ctas_of(ents[order[r0].second]);
-    for (r1 = r0; r1 < ents.size() && r1 - r0 < kMaxRowsPerLaunch; ++r1) {
-      const ScoredEntry &e = ents[order[r1].second];
+    for (size_t j = r0; j < r1; ++j) {
+      const ScoredEntry &e = ents[order[j].second];
       const int q_tiles = ctas_of(e);
       if (q_tiles != p.uniform_tiles) p.uniform_tiles = 0;
-      if (cta + q_tiles > kMaxEntryCtas) break;
-      PrefillRow &r = p.rows[r1 - r0];
+      PrefillRow &r = p.rows[j - r0];
       r = e.row;
       r.cta0 = cta;
       cta += q_tiles;
-      p.prefix[r1 - r0] = e.prefix;
-      p.part0[r1 - r0] = e.part0;
-      p.splits[r1 - r0] = (uint8_t)e.splits;
+      p.prefix[j - r0] = e.prefix;
+      p.part0[j - r0] = e.part0;
+      p.splits[j - r0] = (uint8_t)e.splits;
       if (r.tile0 != 0) continue;  // a row's work is counted with its first entry
       const double keys = stored_keys(e), own = sliding || sa.parents ? e.row.n : 0.0;
       bytes += 4.0 * (keys + own) * Hk * D + 4.0 * r.n * Hq * D;
@@ -3116,6 +3130,7 @@ int attend_scored(kv_cache *c, int layer, const __nv_bfloat16 *q, __nv_bfloat16 
     const cudaError_t e = timed(c, KV_KERNEL_PREFILL, bytes, fl, s,
                                 [&] { return launch_chunk_scored(p, D, s, c->pdl); });
     if (e != cudaSuccess) return KV_ERR_CUDA;
+    r0 = r1;
   }
   return launch_merges(c, merges, out, (int64_t)Hq * D, nullptr, s);
 }
