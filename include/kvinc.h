@@ -610,7 +610,8 @@ int kv_store(kv_cache *c, int layer, const void *k, const void *v, int C, const 
  *          layers only (KV_ERR_ARG otherwise).  Entries of rows without new tokens are not read.
  *
  * A token that sees no key gets zeros.  Keys and values that a token does not see may hold
- * infinities and NaN (all outputs of a token that sees such a value itself may be NaN).  On a
+ * infinities and NaN (all outputs of a token that sees such a value itself may be NaN).  Sums of
+ * values are float32 with weights up to 1: finite ones up to 2^127 / (keys seen) do not overflow.  On a
  * global layer a row with evicted keys takes a cap only (KV_ERR_ARG with slopes, first or prefix:
  * its slots are not its positions).  The global layer's new tokens are all stored before any of
  * them attends, and attend in one launch per 512 rows.  Bs * C < 2^31.  KV_ERR_ARG on a hybrid

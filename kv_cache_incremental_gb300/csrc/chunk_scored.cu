@@ -18,16 +18,16 @@
 // allow, sixteen: four threads per query row, 32 of the block's keys each, which a thread holds
 // in registers from TMEM to TMEM.  The four keep the same maximum; it moves, and O is rescaled,
 // only when a score exceeds it by kRise, on a vote of their warps.  Weights up to 2^kRise cost
-// no accuracy (floats and bf16 halves are relative) and leave 2^95 to the values.
+// no accuracy (floats and bf16 halves are relative), but with values above 2^95 a sum may overflow.
 //
 // Measured: 64 rows of 1k to 8k keys, 4 to 16 drafts, Hq 32, Hk 8, D 128, 195 us: 92% of the
 // copy rate.  16 rows of 16k to 32k keys, 8 to 32 drafts, Hq 64, Hk 8, capped, 475 us: a block
 // takes 2 550 cycles, 2 100 without a cap, its products 1 540; a CTA 15 000 beside its blocks.
 //
 // A hidden key's weight is 0, but 0 times infinity is NaN.  So when an output is not finite, the
-// CTA runs over its blocks a second time with such values set to 0, and the rows that see none
-// of them take that.  (Values are looked at only then: a scan of every tile would be on the
-// chain.)
+// CTA runs over its blocks a second time with such values set to 0 and the maximum exact at every
+// block (weights up to 1), and the rows that see none of them take that.  (Values are looked at only
+// then: a scan of every tile would be on the chain.)
 //
 // A piece of a split row's keys may hold no block for a query tile.  Such a CTA has no MMAs to wait
 // for, so it commits none either: a commit's arrival that nothing waits for could come after the
@@ -57,7 +57,7 @@ constexpr int kPart = 32;         // keys of a softmax thread
 constexpr int kSoftWarps = 16, kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarpK = kSoftWarps, kWarpS = kWarpK + 1, kWarpO = kWarpS + 1, kWarpV = kWarpO + 1;
 constexpr int kThreads = 32 * (kWarpV + 1);  // 20 warps: five per sub-partition, 96 registers
-constexpr float kRise = 32.f;
+constexpr float kRise = 32.f;  // of the first run
 constexpr int kBufs = 3;  // S buffers: one in the softmax, one ahead, one whose P is read
 constexpr int kFar = 1 << 30;  // past any position
 // Named barriers: 1-4 the four warps of 32 query rows, 5-8 of a quarter of the keys, 15 all
@@ -427,7 +427,7 @@ __device__ __forceinline__ __nv_bfloat16 *out_row(const ScoredPrefillParams &p, 
 }
 
 // A softmax warp's run over the blocks, and the rows' outputs.  kClean: the second run, without
-// values that are not finite.
+// values that are not finite and with weights up to 1.
 template <int D, bool kClean>
 __device__ __forceinline__ void softmax_run(const ScoredPrefillParams &p, uint8_t *smem,
                                             Bars<D> bar, uint32_t tmem, const Sees &see) {
@@ -536,7 +536,8 @@ __device__ __forceinline__ void softmax_run(const ScoredPrefillParams &p, uint8_
       // With `top` the largest of the scores: the maximum of the row, then the weights 2^(x -
       // m), x = scaled(v), over the columns of the scores.
       const auto finish = [&](const float (&v)[kPart], float top, auto scaled) {
-        const bool rise = m_used == -INFINITY ? top > -INFINITY : top > m_used + kRise;
+        const bool rise =
+            m_used == -INFINITY ? top > -INFINITY : top > m_used + (kClean ? 0.f : kRise);
         if (bar_any(rows_bar, 128, rise)) {
           *num_mine = top;
           bar_sync(rows_bar, 128);
@@ -545,7 +546,7 @@ __device__ __forceinline__ void softmax_run(const ScoredPrefillParams &p, uint8_
           // (the barrier of the next vote keeps the next exchange apart)
           float alpha = 1.f;
           if (m_used == -INFINITY) m_used = top;  // O and l of this row are still zero
-          else if (top > m_used + 8.f) alpha = exp2f(m_used - top), m_used = top;
+          else if (top > m_used + (kClean ? 0.f : 8.f)) alpha = exp2f(m_used - top), m_used = top;
           if (it > 0) {
             // O of the block before may still run.  (Its barrier's phase before is that of four
             // blocks before this one, done before S of the block before was issued over its P.)
@@ -893,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     see.open1 = end - i0;
   }
 
-  // The runs over the blocks: one, or a second one without the values that are not finite.
+  // The runs over the blocks: one, or a second one when an output is not finite.
   const auto run_blocks = [&](auto clean) {
     constexpr bool kClean = decltype(clean)::value;
     const Bars<D> bar(smem, kClean);
