@@ -11,20 +11,21 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // tanh(x) = x P(x^2) for |x| <= 0.6: P is the polynomial of degree 4 in x^2 with the smallest
-// largest relative error on [0, 0.36] (equal ripples of 7.3e-8, fitted by exchange on tanh itself).
+// largest relative error on [0, 0.36], fitted to tanh itself a coefficient at a time, each rounded to
+// float before the next ones are fitted (7.5e-8; 7.3e-8 unrounded, 9.1e-8 if rounded at the end).
 // A score is that close to its cap only rarely, and while none of a warp's is, the polynomial leaves
 // the special-function unit, which the weights' exponentials keep busy, alone.
 constexpr float kTanhSmall = 0.6f;
 __host__ __device__ constexpr float tanh_coef(int i) {
-  constexpr float c[5] = {0.99999994f, -0.3333231f, 0.13310173f, -0.05210148f, 0.015475428f};
+  constexpr float c[5] = {0.99999994f, -0.3333236f, 0.13310668f, -0.05211966f, 0.015497749f};
   return c[i];
 }
-// And of degree 3 for |x| <= 0.38 (6.6e-8): a cap of 30 has most scores below 11, and a packed product
+// And of degree 3 for |x| <= 0.38 (6.7e-8): a cap of 30 has most scores below 11, and a packed product
 // less per two scores is 5% of a capped block (chunk_scored.cu: 16 rows of 16k to 32k keys, 8 to 32
 // drafts, Hq 64, Hk 8: 500 us with degree 4 alone, 477 with both; degree 2 for |x| <= 0.18 as well, 484).
 constexpr float kTanhTiny = 0.38f;
 __host__ __device__ constexpr float tanh_coef3(int i) {
-  constexpr float c[4] = {0.99999994f, -0.33331868f, 0.13281983f, -0.048131067f};
+  constexpr float c[4] = {0.99999994f, -0.333319f, 0.13282442f, -0.048148867f};
   return c[i];
 }
 __device__ __forceinline__ float tanh_small(float x) {
