@@ -20,9 +20,10 @@
 // only when a score exceeds it by kRise, on a vote of their warps.  Weights up to 2^kRise cost
 // no accuracy (floats and bf16 halves are relative), but with values above 2^95 a sum may overflow.
 //
-// Measured: 64 rows of 1k to 8k keys, 4 to 16 drafts, Hq 32, Hk 8, D 128, 195 us: 92% of the
-// copy rate.  16 rows of 16k to 32k keys, 8 to 32 drafts, Hq 64, Hk 8, capped, 475 us: a block
-// takes 2 550 cycles, 2 100 without a cap, its products 1 540; a CTA 15 000 beside its blocks.
+// Measured: 64 rows of 1k to 8k keys, 4 to 16 drafts, Hq 32, Hk 8, D 128, 196 us: 92% of the
+// copy rate.  16 rows of 16k to 32k keys, 8 to 32 drafts, Hq 64, Hk 8, capped, 463 us.  A block takes
+// 2 700 to 2 800 cycles, 2 000 to 2 200 without a cap, its products 1 540; a CTA 15 000 beside its
+// blocks.
 //
 // A hidden key's weight is 0, but 0 times infinity is NaN.  So when an output is not finite, the
 // CTA runs over its blocks a second time with such values set to 0 and the maximum exact at every

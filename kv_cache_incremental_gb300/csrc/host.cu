@@ -2966,7 +2966,7 @@ struct ScoredEntry {
 constexpr int kMaxEntryTokens = 16384;
 constexpr int kMaxEntryCtas = 32767;
 // Key splits (attend_scored), in blocks of 128 keys: the shortest piece, what a CTA costs beside its
-// blocks (15 000 cycles, a block 2 100 to 2 550), and what a merge adds to the call.
+// blocks (15 000 cycles, a block 2 000 to 2 800), and what a merge adds to the call.
 constexpr int kMinPiece = 2, kPieceCost = 6, kMergeCost = 5;
 
 // Attention of the entries' tokens with changed scores, key splits and their merge included.  The
@@ -3196,7 +3196,11 @@ int chunks_scored_ring(kv_cache *c, int layer, const __nv_bfloat16 *q, const __n
 // is twice as many bytes for the same time.  24 rows of up to 6k keys, Hq 16, Hk 4, D 64, 64
 // tokens: a tenth of single tokens 91 us apart, 82 together, half of them 85 and 82, 0.8 of them
 // (1.65 times the work) 63 and 72; 32 rows of up to 8k keys, Hq 32, Hk 8, D 128, 16 tokens: a tenth
-// 152 and 134, 0.8 (3.4 times the work) 144 and 134.
+// 152 and 134, 0.8 (3.4 times the work) 144 and 134.  Other groups, a tenth / half / 0.8 of the
+// rows single, apart and together: D 64, 24 rows, Hk 4, 64 tokens, groups of 1 61 / 50 / 50 and
+// 56 / 55 / 55 (work 0.07 / 0.98 / 3.3: half of them are joined, 5 us too many), of 8 157 / 99 / 86
+// and 147 / 96 / 82, of 16 268 / 174 / 136 and 252 / 157 / 98; D 128, 32 rows, Hk 8, 16 tokens,
+// groups of 1 144 / 144 / 135 and 127 / 126 / 126, of 8 155 / 183 / 155 and 131 / 128 / 127.
 bool join_singles(const kv_cache *c, const int32_t *n_new, const std::vector<int32_t> &rows) {
   const int rep = c->Hq / c->Hk;
   int64_t singles = 0, chunks = 0;
