@@ -600,7 +600,8 @@ int kv_store(kv_cache *c, int layer, const void *k, const void *v, int C, const 
  * p - W < j too) from its first one on, and the row's prefix:
  *     (j <= p and j >= first[i][t])  or  j < prefix[i].
  *
- *  cap     0 (none) or in [1e-3, 1e5].  Scores are float32: capped ones are within 2^-20 of the cap
+ *  cap     0 (none) or in [1e-3, 1e5].  Scores are float32, of which a cap adds up
+ *          to 2^-20 of itself to the error
  *  slopes  device float [Hq] or NULL, 4-byte aligned
  *  first   device int32 [Bs][C] or NULL (0 everywhere), 4-byte aligned: the first position of
  *          the token's document.  Any value is allowed; above p the token sees its prefix only.
